@@ -39,11 +39,16 @@ bool device_sms(int* sms) {
 }
 
 // Tensor map over one sequence's cache rows: [rows, 256] elements, boxes of
-// (128 bytes of a row) x kTile rows, 128-byte swizzle -- the canonical K-major /
+// (128 bytes of a row) x box_rows rows, 128-byte swizzle -- the canonical K-major /
 // MN-major shared-memory layout of the tensor-core operands.
-bool encode_rows(CUtensorMap* m, void* base, int rows, int dtype) {
+bool encode_rows(CUtensorMap* m, void* base, int rows, int dtype, int box_rows) {
   const int elem = dtype == MFA_KV_FP8_E4M3 ? 1 : 2;
-  return encode_2d(m, base, (uint64_t)rows, kHeadDim, elem, 128 / elem, kTile);
+  return encode_2d(m, base, (uint64_t)rows, kHeadDim, elem, 128 / elem, box_rows);
+}
+
+// a device array of int32
+bool valid_ints(const int32_t* p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 }
 
 mfa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MFA_OK : MFA_ERR_CUDA; }
@@ -286,6 +291,18 @@ bool encode_pool(CUtensorMap* m, const void* base, uint64_t pages, uint64_t page
 
 namespace {
 
+// The KV table to the device: the entries, then the chunk attention's maps where there are.
+mfa_status store_table(void* table, const std::vector<KvSeq>& host,
+                       const std::vector<KvChunkMaps>& maps, cudaStream_t s) {
+  cudaError_t e = cudaMemcpyAsync(table, host.data(), sizeof(KvSeq) * host.size(),
+                                  cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess && !maps.empty())
+    e = cudaMemcpyAsync(static_cast<uint8_t*>(table) + sizeof(KvSeq) * host.size(), maps.data(),
+                        sizeof(KvChunkMaps) * maps.size(), cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return cuda_status(e);
+}
+
 // The attention of one call: the tensor-core kernel, then the merge of split sequences.
 // Unless the plan was launched earlier (aa.plan_early), the attention CTAs build it on chip.
 mfa_status run_attention(const AttnArgs& aa, cudaStream_t s) {
@@ -324,6 +341,11 @@ size_t mfa_kv_table_bytes(int32_t batch) {
   return sizeof(KvSeq) * (size_t)batch;
 }
 
+size_t mfa_chunk_table_bytes(int32_t batch) {
+  if (batch < 1 || batch > kMaxBatch) return 0;
+  return (sizeof(KvSeq) + sizeof(KvChunkMaps)) * (size_t)batch;
+}
+
 mfa_status mfa_kv_table_init(void* table, size_t table_bytes, int32_t batch, int32_t dtype,
                              void* const* k_ptrs, void* const* v_ptrs,
                              const int32_t* capacity, void* stream) {
@@ -339,21 +361,24 @@ mfa_status mfa_kv_table_init(void* table, size_t table_bytes, int32_t batch, int
     if (capacity[b] < 1 || capacity[b] > MFA_MAX_CONTEXT) return MFA_ERR_INVALID_ARG;
   }
   if (encode_tiled_fn() == nullptr) return MFA_ERR_CUDA;
+  const bool chunk = table_bytes >= mfa_chunk_table_bytes(batch);
   std::vector<KvSeq> host(batch);
+  std::vector<KvChunkMaps> maps(chunk ? batch : 0);
   std::memset(host.data(), 0, sizeof(KvSeq) * batch);
   for (int b = 0; b < batch; ++b) {
-    if (!encode_rows(&host[b].tmap_k, k_ptrs[b], capacity[b], dtype) ||
-        !encode_rows(&host[b].tmap_v, v_ptrs[b], capacity[b], dtype))
+    if (!encode_rows(&host[b].tmap_k, k_ptrs[b], capacity[b], dtype, kTile) ||
+        !encode_rows(&host[b].tmap_v, v_ptrs[b], capacity[b], dtype, kTile))
+      return MFA_ERR_INVALID_ARG;
+    if (chunk &&
+        (!encode_rows(&maps[b].k, k_ptrs[b], capacity[b], dtype, kChunkBoxRows) ||
+         !encode_rows(&maps[b].v, v_ptrs[b], capacity[b], dtype, kChunkBoxRows)))
       return MFA_ERR_INVALID_ARG;
     host[b].k = k_ptrs[b];
     host[b].v = v_ptrs[b];
     host[b].capacity = capacity[b];
+    host[b].chunk_maps = chunk;
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemcpyAsync(table, host.data(), sizeof(KvSeq) * batch,
-                                  cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return cuda_status(e);
+  return store_table(table, host, maps, static_cast<cudaStream_t>(stream));
 }
 
 mfa_status mfa_kv_table_init_paged(void* table, size_t table_bytes, int32_t batch,
@@ -388,20 +413,25 @@ mfa_status mfa_kv_table_init_paged(void* table, size_t table_bytes, int32_t batc
       !encode_pool(&proto.tmap_v, v_pool, num_pages, page_size, elem,
                    paged_box_rows(page_size)))
     return MFA_ERR_INVALID_ARG;
+  const bool chunk = table_bytes >= mfa_chunk_table_bytes(batch);
+  KvChunkMaps proto_maps;
+  std::memset(&proto_maps, 0, sizeof(proto_maps));
+  if (chunk &&
+      (!encode_pool(&proto_maps.k, k_pool, num_pages, page_size, elem, kChunkBoxRows) ||
+       !encode_pool(&proto_maps.v, v_pool, num_pages, page_size, elem, kChunkBoxRows)))
+    return MFA_ERR_INVALID_ARG;
   proto.k = k_pool;
   proto.v = v_pool;
   proto.page_size = page_size;
   proto.num_pages = num_pages;
+  proto.chunk_maps = chunk;
   std::vector<KvSeq> host(batch, proto);
+  const std::vector<KvChunkMaps> maps(chunk ? batch : 0, proto_maps);
   for (int b = 0; b < batch; ++b) {
     host[b].capacity = pages_per_seq[b] * page_size;
     host[b].pages = page_table + (size_t)b * max_pages;
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemcpyAsync(table, host.data(), sizeof(KvSeq) * batch,
-                                  cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return cuda_status(e);
+  return store_table(table, host, maps, static_cast<cudaStream_t>(stream));
 }
 
 size_t mfa_workspace_bytes(int32_t batch) {
@@ -409,6 +439,13 @@ size_t mfa_workspace_bytes(int32_t batch) {
   int sms = 0;
   if (!device_sms(&sms)) return 0;
   return ws_layout(batch, sms).total;
+}
+
+size_t mfa_chunk_workspace_bytes(int32_t batch) {
+  if (batch < 1 || batch > kMaxBatch) return 0;
+  int sms = 0;
+  if (!device_sms(&sms)) return 0;
+  return chunk_ws_bytes(ws_layout(batch, sms), sms);
 }
 
 mfa_status mfa_workspace_init(void* ws, size_t ws_bytes, void* stream) {
@@ -522,6 +559,97 @@ mfa_status mfa_decode_attn(const void* q, const mfa_kv_cache* kv, const int32_t*
   aa.grid = L.attn_grid;
   aa.page_size = kv->page_size;
   return run_attention(aa, static_cast<cudaStream_t>(stream));
+}
+
+mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, const void* v,
+                           int32_t v_ld, const mfa_rope* rope, const int32_t* positions,
+                           const mfa_kv_cache* kv, const int32_t* q_start,
+                           const int32_t* seq_lens, int32_t n_rows, void* q_out, void* ws,
+                           size_t ws_bytes, void* stream) {
+  mfa_status st = check_kv(kv);
+  if (st != MFA_OK) return st;
+  if (n_rows < 1 || n_rows > MFA_MAX_ROWS) return MFA_ERR_INVALID_ARG;
+  if (k_ld < kHeadDim || k_ld % 8 != 0 || v_ld < kHeadDim || v_ld % 8 != 0)
+    return MFA_ERR_INVALID_ARG;
+  const void* ptrs[] = {k, v};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return MFA_ERR_INVALID_ARG;
+  if (!valid_ints(q_start) || !valid_ints(seq_lens)) return MFA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return MFA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out)) return MFA_ERR_INVALID_ARG;
+  RopeAppendArgs a{};
+  if (rope != nullptr) {
+    if (rope->table == nullptr || !aligned16(rope->table) || rope->max_pos < 1)
+      return MFA_ERR_INVALID_ARG;
+    if (rope->rot_dim < 16 || rope->rot_dim > kHeadDim || rope->rot_dim % 16 != 0)
+      return MFA_ERR_INVALID_ARG;
+    if (rope->n_axes < 1 || rope->n_axes > 4) return MFA_ERR_INVALID_ARG;
+    if (positions == nullptr ? rope->n_axes != 1 : !valid_ints(positions))
+      return MFA_ERR_INVALID_ARG;
+    for (int i = 0; i < rope->rot_dim / 2; ++i)
+      if (rope->pair_axis[i] >= rope->n_axes) return MFA_ERR_INVALID_ARG;
+    a.table = rope->table;
+    a.max_pos = rope->max_pos;
+    a.rot_dim = rope->rot_dim;
+    a.interleaved = rope->interleaved != 0;
+    std::memcpy(a.pair_axis, rope->pair_axis, sizeof(a.pair_axis));
+  } else if (q != nullptr || positions != nullptr) {
+    return MFA_ERR_INVALID_ARG;
+  }
+  WsLayout L;
+  st = check_ws(ws, ws_bytes, kv->batch, &L);
+  if (st != MFA_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_ld = k_ld;
+  a.v_ld = v_ld;
+  a.positions = positions;
+  a.kv = static_cast<const KvSeq*>(kv->table);
+  a.kv_dtype = kv->dtype;
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  a.q_start = q_start;
+  a.seq_lens = seq_lens;
+  a.batch = kv->batch;
+  a.n_rows = n_rows;
+  a.err = at<uint32_t>(ws, L.err);
+  return cuda_status(launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* q_start,
+                          const int32_t* seq_lens, int32_t n_rows, float scale, void* out,
+                          void* ws, size_t ws_bytes, void* stream) {
+  mfa_status st = check_kv(kv);
+  if (st != MFA_OK) return st;
+  if (n_rows < 1 || n_rows > MFA_MAX_ROWS || !(scale > 0.f)) return MFA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, out};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return MFA_ERR_INVALID_ARG;
+  if (!valid_ints(q_start) || !valid_ints(seq_lens)) return MFA_ERR_INVALID_ARG;
+  WsLayout L;
+  st = check_ws(ws, ws_bytes, kv->batch, &L);
+  if (st != MFA_OK) return st;
+  int sms = 0;
+  if (!device_sms(&sms)) return MFA_ERR_CUDA;
+  if (ws_bytes < chunk_ws_bytes(L, sms)) return MFA_ERR_WORKSPACE;
+  ChunkAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.kv = static_cast<const KvSeq*>(kv->table);
+  a.kv_dtype = kv->dtype;
+  a.page_size = kv->page_size;
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  a.q_start = q_start;
+  a.seq_lens = seq_lens;
+  a.batch = kv->batch;
+  a.n_rows = n_rows;
+  a.scale = scale;
+  a.out = static_cast<uint16_t*>(out);
+  a.partials = at<float>(ws, L.total);
+  a.err = at<uint32_t>(ws, L.err);
+  return cuda_status(launch_chunk_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
 mfa_status mfa_o_proj(const void* out, const void* w_o, void* y, int32_t batch, void* ws,

@@ -52,9 +52,18 @@ struct alignas(128) KvSeq {
   int32_t page_size;      // 0: contiguous
   const int32_t* pages;   // paged: this sequence's row of the page table (device)
   int32_t num_pages;      // paged: pages in each pool
-  int32_t reserved[23];
+  int32_t chunk_maps;     // 1: the table goes on with a KvChunkMaps per sequence
+  int32_t reserved[22];
 };
 static_assert(sizeof(KvSeq) == 384, "KvSeq layout");
+
+// The chunk attention's tensor maps of one sequence: as KvSeq's, with boxes of 64 rows. They
+// follow the KvSeq entries of a table of mfa_chunk_table_bytes bytes.
+struct alignas(128) KvChunkMaps {
+  CUtensorMap k;
+  CUtensorMap v;
+};
+constexpr int kChunkBoxRows = 64;
 
 // The element row, in its K or V buffer (or pool), of cache row `row` of sequence s: the
 // sequence's own row, or for a paged cache row % page_size of page pages[row / page_size].
@@ -133,6 +142,17 @@ inline WsLayout ws_layout(int batch, int num_sms) {
   off = align_up(off + sizeof(float) * (size_t)batch * (kRank / 128), 256);
   L.total = off;
   return L;
+}
+
+// The chunk attention's partials follow the workspace of the other calls: its work is cut
+// into contiguous ranges over pairs of SMs, and a range has at most two items that end inside
+// a tile, its first and its last (chunk_attn.cu), so two slots of 256 rows -- 4 tokens x 64
+// heads, running maximum and sum and the 256 accumulators of each, fp32 -- per pair.
+constexpr int kChunkRows = 256;
+constexpr size_t kChunkPartialFloats = (size_t)kChunkRows * (2 + kHeadDim);
+inline int chunk_grid_for(int num_sms) { return num_sms / 2; }
+inline size_t chunk_ws_bytes(const WsLayout& L, int num_sms) {
+  return L.total + 2 * (size_t)chunk_grid_for(num_sms) * kChunkPartialFloats * sizeof(float);
 }
 
 // Launch with programmatic stream serialization: the kernel may start while the previous
@@ -251,6 +271,42 @@ size_t attention_tc_smem_bytes();
 // launched right after launch_attention_tc on the same stream, as its programmatic
 // dependent.
 cudaError_t launch_attention_combine(const AttnArgs& a, cudaStream_t s);
+
+struct RopeAppendArgs {
+  const uint16_t* q;        // [n_rows, 64, 256] bf16, or null (append only)
+  uint16_t* q_out;
+  const uint16_t* k;        // row t at k + t * k_ld
+  const uint16_t* v;
+  int k_ld, v_ld;
+  const float* table;       // [max_pos, rot_dim]: cosines, then sines
+  int max_pos, rot_dim;     // rot_dim 0: no rotation
+  int interleaved;
+  const int32_t* positions; // [axes, n_rows], or null: the cache row
+  uint8_t pair_axis[kHeadDim / 2];
+  const KvSeq* kv;
+  int kv_dtype;
+  float k_scale, v_scale;
+  const int32_t* q_start;   // [batch + 1]
+  const int32_t* seq_lens;  // [batch]
+  int batch, n_rows;
+  uint32_t* err;
+};
+cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s);
+
+struct ChunkAttnArgs {
+  const uint16_t* q;        // [n_rows, 64, 256] bf16
+  const KvSeq* kv;          // device table
+  int kv_dtype, page_size;
+  float k_scale, v_scale;   // FP8 only
+  const int32_t* q_start;   // [batch + 1]
+  const int32_t* seq_lens;  // [batch]
+  int batch, n_rows;
+  float scale;
+  uint16_t* out;            // [n_rows, 64, 256] bf16
+  float* partials;
+  uint32_t* err;
+};
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t s);
 
 // One CTA whose bounded wait on a barrier that nothing completes gives up after limit_us
 // and sets kErrTimeout in *err (selftest.cu).

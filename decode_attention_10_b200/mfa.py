@@ -22,6 +22,16 @@ STATUS = {0: "MFA_OK", 1: "MFA_ERR_INVALID_ARG", 2: "MFA_ERR_UNSUPPORTED",
           3: "MFA_ERR_CAPACITY", 4: "MFA_ERR_WORKSPACE", 5: "MFA_ERR_CUDA",
           6: "MFA_ERR_EMPTY", 7: "MFA_ERR_TIMEOUT"}
 
+MAX_ROWS = 4194304
+
+
+class RopeDesc(ctypes.Structure):
+    """mfa_rope."""
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * (HEAD_DIM // 2))]
+
+
 class W8(ctypes.Structure):
     """mfa_w8: a block-FP8 weight (device pointers to codes and scales)."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
@@ -33,6 +43,12 @@ _SIGNATURES = {
     "mfa_version": (ctypes.c_int32, []),
     "mfa_status_str": (ctypes.c_char_p, [ctypes.c_int32]),
     "mfa_kv_table_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "mfa_chunk_table_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "mfa_chunk_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "mfa_rope_append": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, ctypes.c_int32, _P, _P, _P,
+                                       _P, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
+    "mfa_chunk_attn": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, _P, _P,
+                                      ctypes.c_size_t, _P]),
     "mfa_kv_table_init": (ctypes.c_int, [_P, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int32,
                                          _P, _P, _P, _P]),
     "mfa_kv_table_init_paged": (ctypes.c_int, [_P, ctypes.c_size_t, ctypes.c_int32,
@@ -158,7 +174,7 @@ class KVCache:
         self.capacity = caps
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         dev = self.k[0].device
-        nbytes = lib.mfa_kv_table_bytes(self.batch)
+        nbytes = lib.mfa_chunk_table_bytes(self.batch)
         if nbytes == 0:
             raise ValueError(f"batch {self.batch} out of range")
         self.table = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -204,7 +220,7 @@ class PagedKVCache:
         self.pages_per_seq = pps
         self.capacity = [n * self.page_size for n in pps]
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
-        nbytes = lib.mfa_kv_table_bytes(self.batch)
+        nbytes = lib.mfa_chunk_table_bytes(self.batch)
         if nbytes == 0:
             raise ValueError(f"batch {self.batch} out of range")
         self.table = torch.empty(nbytes, dtype=torch.uint8, device=k_pool.device)
@@ -239,10 +255,12 @@ class BlockFP8Weight:
 class Workspace:
     """Device workspace for `batch` sequences (allocated by torch, zeroed by the library)."""
 
+    _bytes = staticmethod(lambda lib, batch: lib.mfa_workspace_bytes(batch))
+
     def __init__(self, batch: int, device=None, stream: Optional[torch.cuda.Stream] = None):
         lib = load()
         self.batch = int(batch)
-        self.nbytes = lib.mfa_workspace_bytes(self.batch)
+        self.nbytes = self._bytes(lib, self.batch)
         if self.nbytes == 0:
             raise ValueError(f"batch {batch} out of range (or no CUDA device)")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8,
@@ -253,6 +271,44 @@ class Workspace:
     @property
     def ptr(self) -> int:
         return self.buf.data_ptr()
+
+
+class ChunkWorkspace(Workspace):
+    """A workspace for chunk_attn as well as every other call on `batch` sequences."""
+
+    _bytes = staticmethod(lambda lib, batch: lib.mfa_chunk_workspace_bytes(batch))
+
+
+def rope_table(max_pos: int, rot_dim: int = HEAD_DIM, base: float = 10000.0, scale: float = 1.0,
+               device=None) -> torch.Tensor:
+    """The table of a Rope: float32 [max_pos, rot_dim], cosines and sines of the angles
+    scale * p * base^(-2 i / rot_dim), i < rot_dim / 2, formed in float64 (a float32 angle of
+    position 65535 is off by up to 2^-9 radians)."""
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    ang = scale * torch.arange(max_pos, dtype=torch.float64)[:, None] * base ** (-2.0 * i / rot_dim)
+    return torch.cat([ang.cos(), ang.sin()], 1).to(torch.float32).to(device or "cuda")
+
+
+class Rope:
+    """A rotary position embedding described to the library (mfa_rope): `table` from
+    rope_table, or any CUDA float32 [max_pos, rot_dim] of cosines and sines. pair_axis gives
+    the axis of each of the rot_dim / 2 pairs (None: all on axis 0), for positions on several
+    axes: sections (16, 24, 24) of time, height and width are [0] * 16 + [1] * 24 + [2] * 24.
+    Keeps a reference to the table."""
+
+    def __init__(self, table: torch.Tensor, pair_axis: Optional[Sequence[int]] = None,
+                 interleaved: bool = False):
+        if table.dim() != 2 or table.dtype != torch.float32:
+            raise ValueError("table must be float32 [max_pos, rot_dim]")
+        self.table, self.rot_dim = table, int(table.shape[1])
+        if self.rot_dim % 16 != 0 or not 16 <= self.rot_dim <= HEAD_DIM:
+            raise ValueError("rot_dim must be a multiple of 16, 16 .. 256")
+        axes = [0] * (self.rot_dim // 2) if pair_axis is None else [int(a) for a in pair_axis]
+        if len(axes) != self.rot_dim // 2 or min(axes) < 0 or max(axes) > 3:
+            raise ValueError("pair_axis needs an axis 0 .. 3 for each of the rot_dim / 2 pairs")
+        self.n_axes = max(axes) + 1
+        self.desc = RopeDesc(_ptr(table), int(table.shape[0]), self.rot_dim, int(interleaved),
+                             self.n_axes, (ctypes.c_uint8 * (HEAD_DIM // 2))(*axes))
 
 
 def get_error(ws: Workspace, stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -311,6 +367,80 @@ def decode_layer(x, w_qdown, gamma, w_qup, w_k, w_v, cache: KVCache, seq_lens,
                                 ws.nbytes, _stream(stream)),
            "mfa_decode_layer")
     return q_out, out
+
+
+def _token_batch(cache, q_start: torch.Tensor, seq_lens: torch.Tensor):
+    """Checks of a ragged batch's two arrays."""
+    for t, n, what in ((q_start, cache.batch + 1, "q_start"), (seq_lens, cache.batch, "seq_lens")):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
+            raise ValueError(f"{what} must be int32 [{n}]")
+
+
+def _rows(t: torch.Tensor, n_rows: int, what: str):
+    """A [n_rows, 256] bf16 CUDA tensor whose rows may lie apart: its pointer and row stride."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n_rows, HEAD_DIM) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA bf16 [{n_rows}, {HEAD_DIM}]")
+    if t.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be dense")
+    return t.data_ptr(), t.stride(0) if n_rows > 1 else max(HEAD_DIM, t.stride(0) // 8 * 8)
+
+
+def _queries(t: torch.Tensor, n_rows: int, what: str) -> int:
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n_rows, N_HEADS, HEAD_DIM):
+        raise ValueError(f"{what} must be bf16 [{n_rows}, {N_HEADS}, {HEAD_DIM}]")
+    return _ptr(t)
+
+
+def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
+                rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                q_out=None, ws=None, stream=None) -> Optional[torch.Tensor]:
+    """mfa_rope_append: rotate the queries q [T, 64, 256] (or None) and keys k [T, 256] of a
+    ragged batch of new tokens and append k and v to the cache; returns the rotated queries
+    (q_out; q itself may be given). Rows q_start[b] .. q_start[b + 1] are sequence b's, the
+    last of its seq_lens[b] positions; k and v may be views with spaced rows. positions: int32
+    [axes, T] or [T]; None: a token's cache row."""
+    lib = load()
+    n = int(k.shape[0])
+    _token_batch(cache, q_start, seq_lens)
+    kp, k_ld = _rows(k, n, "k")
+    vp, v_ld = _rows(v, n, "v")
+    qp = qop = None
+    if q is not None:
+        qp = _queries(q, n, "q")
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        qop = _queries(q_out, n, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if positions is not None:
+        axes = rope.n_axes if rope is not None else 0
+        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) \
+                or positions.numel() != axes * n or positions.shape[-1] != n:
+            raise ValueError(f"positions must be int32 [{axes}, {n}]")
+    ws = ws if ws is not None else Workspace(cache.batch, k.device)
+    _check(lib.mfa_rope_append(qp, kp, k_ld, vp, v_ld,
+                               ctypes.byref(rope.desc) if rope is not None else None,
+                               _ptr(positions), ctypes.byref(cache.desc), _ptr(q_start),
+                               _ptr(seq_lens), n, qop, ws.ptr, ws.nbytes, _stream(stream)),
+           "mfa_rope_append")
+    return q_out
+
+
+def chunk_attn(q, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
+               scale: float = 1.0 / 16.0, out=None, ws=None, stream=None) -> torch.Tensor:
+    """mfa_chunk_attn: causal attention of a ragged batch of new tokens q [T, 64, 256] over the
+    cache (which holds their keys and values already); rows as in rope_append. Rows of no
+    sequence are left as they were in `out`. ws: a ChunkWorkspace."""
+    lib = load()
+    n = int(q.shape[0])
+    _token_batch(cache, q_start, seq_lens)
+    if out is None:
+        out = torch.empty_like(q)
+    ws = ws if ws is not None else ChunkWorkspace(cache.batch, q.device)
+    _check(lib.mfa_chunk_attn(_queries(q, n, "q"), ctypes.byref(cache.desc), _ptr(q_start),
+                              _ptr(seq_lens), n, float(scale), _queries(out, n, "out"), ws.ptr,
+                              ws.nbytes, _stream(stream)), "mfa_chunk_attn")
+    return out
 
 
 def o_proj(out, w_o, y=None, ws=None, stream=None) -> torch.Tensor:

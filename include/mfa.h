@@ -105,6 +105,12 @@ MFA_API const char* mfa_status_str(int32_t status);
 /* Bytes of the device KV table for `batch` sequences (0 if batch is out of range). */
 MFA_API size_t mfa_kv_table_bytes(int32_t batch);
 
+/* Bytes of a device KV table that mfa_chunk_attn can read as well (0 if batch is out of
+ * range): a table that mfa_kv_table_init / _paged is given at least this many bytes for also
+ * gets the tensor maps of the chunk attention, 256 bytes a sequence, behind the entries that
+ * the decode calls read. */
+MFA_API size_t mfa_chunk_table_bytes(int32_t batch);
+
 /* Describe a KV cache to the library. For each sequence b: k_ptrs[b] and v_ptrs[b] are
  * device base addresses of its K and V rows, each [capacity[b], 256] elements of `dtype`,
  * row-major, 16-byte aligned (sequences may live in separate allocations or be slices of
@@ -147,6 +153,11 @@ MFA_API mfa_status mfa_kv_table_init_paged(void* table, size_t table_bytes, int3
  * device (0 if batch is out of range). One workspace must not be used by two calls that
  * can run at the same time. */
 MFA_API size_t mfa_workspace_bytes(int32_t batch);
+
+/* Bytes of a workspace that serves mfa_chunk_attn as well as every other call for `batch`
+ * sequences (0 if batch is out of range): mfa_workspace_bytes(batch) and the chunk
+ * attention's partials (39 MB on 148 SMs). */
+MFA_API size_t mfa_chunk_workspace_bytes(int32_t batch);
 
 /* Zero a freshly allocated workspace (device buffer, 256-byte aligned) on `stream` and
  * wait. Needed once per allocation: the compute calls leave it ready for the next call. */
@@ -258,6 +269,83 @@ MFA_API mfa_status mfa_decode_layer_w8(const void* x, mfa_w8 w_qdown, const void
  * WORKSPACE (ws too small), CUDA (launch failure). */
 MFA_API mfa_status mfa_o_proj(const void* out, const void* w_o, void* y, int32_t batch,
                               void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Chunks of new tokens (prompts, chunked prompts, drafted tokens, mixed batches)
+ * ------------------------------------------------------------------------------------- */
+
+/* A ragged batch of new tokens, as the two calls below take it: the tokens of all sequences
+ * are rows 0 .. n_rows - 1 of q, k, v and out, in order; sequence b owns rows q_start[b] ..
+ * q_start[b + 1] - 1, n_b = q_start[b + 1] - q_start[b] of them (0: the sequence has no new
+ * token and is left alone). seq_lens[b] counts the sequence's positions AFTER the append, so
+ * its new tokens are positions seq_lens[b] - n_b .. seq_lens[b] - 1.
+ *   q_start: device int32 [kv->batch + 1], nondecreasing, 0 <= q_start[0], q_start[kv->batch]
+ *   <= n_rows; rows before q_start[0] or from q_start[kv->batch] on belong to no sequence:
+ *   they are not read as tokens and their outputs are left as they were.
+ *   seq_lens: device int32 [kv->batch], n_b <= seq_lens[b] <= capacity[b].
+ *   n_rows: 1 .. MFA_MAX_ROWS. Both arrays are read on the device at every call. */
+#define MFA_MAX_ROWS 4194304
+
+/* Rotary position embedding. A row's first rot_dim dimensions are rotated in pairs; pair i
+ * (i < rot_dim / 2) is dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),  cos = table[p][i], sin = table[p][rot_dim / 2 + i]
+ * with p the token's position on axis pair_axis[i]. One axis is ordinary text; several axes
+ * (time, height, width) are images and video, each pair following the axis it is given. The
+ * Step-3 pages state no positional encoding: the rotation is an option of these calls, and
+ * the layer step above has none. */
+typedef struct {
+  const float* table;      /* device float32 [max_pos, rot_dim], 16-byte aligned: per position
+                              the cosines, then the sines, of its rot_dim / 2 angles */
+  int32_t max_pos;         /* rows of the table, >= 1 */
+  int32_t rot_dim;         /* a multiple of 16, 16 .. 256; the other dimensions stay */
+  int32_t interleaved;     /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+  int32_t n_axes;          /* 1 .. 4 */
+  uint8_t pair_axis[MFA_HEAD_DIM / 2]; /* axis of each pair, < n_axes */
+} mfa_rope;
+
+/* Rotate the queries and keys of a chunk of new tokens and append its keys and values to the
+ * cache, in one pass:
+ *   q_out = bf16(R(p) q);  K row j <- bf16(R(p) k), V row j <- bf16(v), or for FP8 caches
+ *   e4m3(R(p) k / k_scale) and e4m3(v / v_scale),  j the token's position in its sequence.
+ * The rotation runs in float32 and is rounded once.
+ *   q: device bf16 [n_rows, 64, 256] or NULL (append only); q_out: as q, or q itself.
+ *   k, v: device bf16, row t at element t * k_ld (v_ld); k_ld and v_ld are multiples of 8,
+ *   at least 256, so that k and v may be halves of one projection's output.
+ *   rope: host pointer, NULL = no rotation (then q must be NULL: nothing would happen to it).
+ *   positions: device int32 [rope->n_axes, n_rows], or NULL for rope->n_axes == 1: the
+ *   position of a token is then its cache row j. NULL without rope.
+ *   ws: a workspace of mfa_workspace_bytes or mfa_chunk_workspace_bytes(kv->batch) bytes;
+ *   only its error word is used.
+ * A token whose row j or page lies outside the cache, or whose position is outside
+ * [0, max_pos), writes nothing (neither q_out nor the cache) and sets MFA_ERR_CAPACITY; so
+ * does every token of a sequence with seq_lens[b] < n_b that would fall on a negative row.
+ * Only the appended rows of the cache are written. */
+MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, const void* v,
+                                   int32_t v_ld, const mfa_rope* rope, const int32_t* positions,
+                                   const mfa_kv_cache* kv, const int32_t* q_start,
+                                   const int32_t* seq_lens, int32_t n_rows, void* q_out,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* Causal attention of a chunk of new tokens over the cache, which holds their keys and values
+ * already (mfa_rope_append or mfa_kv_append):
+ *   out[t][h] = sum_{j <= p_t} softmax_j(scale * q[t][h] . K_b[j]) V_b[j],
+ * p_t the position of token t in its sequence b. With one new token per sequence it is
+ * mfa_decode_attn; long and short chunks may share a call. Cache rows that a token does not
+ * see (later tokens, rows past the sequence's end) may hold any bytes, infinities and NaN
+ * included, and do not reach its result. For FP8 caches the cached codes are used exactly, q
+ * and the softmax weights as in mfa_decode_attn (q with one power-of-two scale per token and
+ * head).
+ * q: device bf16 [n_rows, 64, 256]; out: device bf16 [n_rows, 64, 256]; scale > 0.
+ * kv: a table of mfa_chunk_table_bytes(kv->batch) bytes or more.
+ * ws: device workspace of mfa_chunk_workspace_bytes(kv->batch) bytes (initialized once).
+ * A sequence with seq_lens[b] > capacity[b] (MFA_ERR_CAPACITY), with 0 <= seq_lens[b] < n_b
+ * (MFA_ERR_EMPTY: a token without positions), or with q_start[b] .. q_start[b + 1] not a
+ * range of [0, n_rows) (MFA_ERR_INVALID_ARG) is not computed; its rows of out, where it has
+ * any, are zero-filled. A table without the chunk attention's maps, or of another layout than
+ * kv->page_size, leaves out untouched and sets MFA_ERR_INVALID_ARG. */
+MFA_API mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* q_start,
+                                  const int32_t* seq_lens, int32_t n_rows, float scale,
+                                  void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * Without a caller-provided workspace

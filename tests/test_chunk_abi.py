@@ -1,0 +1,141 @@
+"""The chunk calls without a GPU: arguments that are refused before any device work, table and
+workspace sizes, and the plain forms that the GPU tests compare with."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import chunk_util as cu
+from decode_attention_10_b200 import mfa
+from oracle import mfa as omfa
+
+P = ctypes.c_void_p
+FAKE = P(4096)  # never dereferenced: every call below fails its checks on the host
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from decode_attention_10_b200 import build
+    build.build()
+    return mfa.load()
+
+
+def kv(batch=4, dtype=0, k=1.0, v=1.0, table=4096, page=0):
+    return ctypes.byref(mfa.KvCacheDesc(batch, dtype, k, v, table, page))
+
+
+def test_table_sizes(lib):
+    assert lib.mfa_chunk_table_bytes(0) == 0 == lib.mfa_chunk_table_bytes(mfa.MAX_BATCH + 1)
+    for b in (1, 16, mfa.MAX_BATCH):
+        assert lib.mfa_chunk_table_bytes(b) == lib.mfa_kv_table_bytes(b) + 256 * b
+    assert lib.mfa_chunk_workspace_bytes(0) == 0 == lib.mfa_chunk_workspace_bytes(1025)
+
+
+def test_chunk_attention_refusals(lib):
+    def call(q=FAKE, c=None, starts=FAKE, lens=FAKE, n=5, scale=0.0625, out=FAKE, ws=FAKE,
+             size=BIG):
+        return lib.mfa_chunk_attn(q, c if c is not None else kv(), starts, lens, n, scale, out,
+                                  ws, size, None)
+
+    for bad in (dict(q=None), dict(q=P(4104)), dict(out=None), dict(out=P(4100)),
+                dict(starts=None), dict(starts=P(4098)), dict(lens=None), dict(lens=P(4097)),
+                dict(n=0), dict(n=-1), dict(n=mfa.MAX_ROWS + 1), dict(scale=0.0),
+                dict(scale=-1.0), dict(scale=math.nan), dict(ws=None), dict(ws=P(4096 + 16)),
+                dict(c=kv(batch=0)), dict(c=kv(batch=1025)), dict(c=kv(table=None)),
+                dict(c=kv(table=4096 + 64)), dict(c=kv(page=96)), dict(c=kv(page=32)),
+                dict(c=kv(dtype=1, k=0.0)), dict(c=kv(dtype=1, v=-1.0))):
+        assert call(**bad) == 1, bad
+    assert lib.mfa_chunk_attn(FAKE, None, FAKE, FAKE, 5, 0.0625, FAKE, FAKE, BIG, None) == 1
+    assert call(c=kv(dtype=2)) == 2
+
+
+def test_rope_append_refusals(lib):
+    def rope(table=4096, max_pos=10, rot=256, inter=0, axes=1, pair=0):
+        return mfa.RopeDesc(table, max_pos, rot, inter, axes, (ctypes.c_uint8 * 128)(*[pair] * 128))
+
+    def call(q=FAKE, k=FAKE, k_ld=256, v=FAKE, v_ld=256, r=rope(), pos=None, c=None,
+             starts=FAKE, lens=FAKE, n=5, out=FAKE, ws=FAKE):
+        return lib.mfa_rope_append(q, k, k_ld, v, v_ld, ctypes.byref(r) if r else None, pos,
+                                   c if c is not None else kv(), starts, lens, n, out, ws, BIG,
+                                   None)
+
+    for bad in (dict(k=None), dict(k=P(4100)), dict(v=None), dict(v=P(4104)), dict(k_ld=255),
+                dict(k_ld=260), dict(v_ld=128), dict(v_ld=257), dict(q=None), dict(out=None),
+                dict(q=P(4104)), dict(out=P(4104)), dict(starts=None), dict(lens=None),
+                dict(starts=P(4098)), dict(n=0), dict(n=mfa.MAX_ROWS + 1), dict(r=None),
+                dict(r=rope(table=None)), dict(r=rope(table=4100)), dict(r=rope(max_pos=0)),
+                dict(r=rope(rot=0)), dict(r=rope(rot=8)), dict(r=rope(rot=24)),
+                dict(r=rope(rot=272)), dict(r=rope(axes=0)), dict(r=rope(axes=5), pos=FAKE),
+                dict(r=rope(axes=2)),  # several axes need positions
+                dict(r=rope(axes=2, pair=2), pos=FAKE), dict(pos=P(4097)), dict(ws=None),
+                dict(c=kv(batch=0)), dict(c=kv(dtype=1, k=0.0)),
+                dict(q=None, out=None, r=None, pos=FAKE)):
+        assert call(**bad) == 1, bad
+    assert call(c=kv(dtype=9)) == 2
+
+
+def test_binding_refusals():
+    cache = type("C", (), {"batch": 2})()
+    starts, lens = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros(4, 64, 256, dtype=torch.bfloat16)
+    kv = torch.zeros(4, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q_start"):
+        mfa.chunk_attn(q, cache, starts[:2], lens, ws=1)
+    with pytest.raises(ValueError, match="seq_lens"):
+        mfa.chunk_attn(q, cache, starts, lens.long(), ws=1)
+    for bad in (q.float(), q[:, :32], q.view(4, 256, 64)):
+        with pytest.raises(ValueError, match="q must be"):
+            mfa.chunk_attn(bad, cache, starts, lens, out=q, ws=mfa)
+    with pytest.raises(ValueError, match="CUDA"):
+        mfa.chunk_attn(q, cache, starts, lens, out=q, ws=mfa)
+    with pytest.raises(ValueError, match="k must be"):
+        mfa.rope_append(q, kv[:, :256], kv[:, 256:], cache, starts, lens, ws=1)
+    with pytest.raises(ValueError, match="rot_dim"):
+        mfa.Rope(torch.zeros(5, 24))
+    with pytest.raises(ValueError, match="float32"):
+        mfa.Rope(torch.zeros(5, 32, dtype=torch.float64))
+    for axes in ([0] * 15, [0] * 15 + [4], [-1] * 16):
+        with pytest.raises(ValueError, match="pair_axis"):
+            mfa.Rope(torch.zeros(5, 32), axes)
+    # what the binding passes on: a table of the wrong place
+    with pytest.raises(ValueError, match="CUDA"):
+        mfa.Rope(torch.zeros(5, 32))
+
+
+def test_rope_table_on_the_cpu():
+    t = mfa.rope_table(300, 32, base=500.0, scale=0.5, device="cpu")
+    for p in (0, 1, 7, 299):
+        for i in range(16):
+            ang = 0.5 * p * 500.0 ** (-2 * i / 32)
+            assert abs(float(t[p, i]) - math.cos(ang)) <= 2.0 ** -24
+            assert abs(float(t[p, 16 + i]) - math.sin(ang)) <= 2.0 ** -24
+
+
+def test_plain_attention_is_the_oracle_s():
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(3, 64, 256, generator=g, dtype=torch.float64)
+    k, v = (torch.randn(9, 256, generator=g, dtype=torch.float64) for _ in range(2))
+    out, mag = cu.attention(q, k, v, 6, 1 / 16)
+    for i in range(3):
+        want = omfa.decode_attn_seq(q[i].numpy(), k[:7 + i].numpy(), v[:7 + i].numpy(), 1 / 16)
+        assert abs(out[i].numpy() - want).max() < 1e-12
+    assert (mag >= out.abs() - 1e-12).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_plain_rotation_turns_pairs(interleaved):
+    # as complex numbers: pair i is multiplied by e^{i angle}; the rest stays
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(5, 3, 256, generator=g, dtype=torch.float64)
+    ang = torch.randn(5, 24, generator=g, dtype=torch.float64)
+    y = cu.rotate(x, ang.cos(), ang.sin(), interleaved)
+    for i in range(24):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, 24 + i)
+        z = torch.complex(x[..., a], x[..., b]) * torch.polar(torch.ones(5, dtype=torch.float64),
+                                                               ang[:, i])[:, None]
+        assert (y[..., a] - z.real).abs().max() < 1e-12
+        assert (y[..., b] - z.imag).abs().max() < 1e-12
+    assert torch.equal(y[..., 48:], x[..., 48:])

@@ -1,0 +1,319 @@
+"""The attention of a chunk of new tokens (mfa_chunk_attn) against its plain form in 64 bits,
+at the lengths, layouts and masks where it can go wrong."""
+
+import pytest
+import torch
+
+from chunk_util import DIM, HEADS, Batch, check
+
+pytestmark = pytest.mark.gpu
+
+KV = pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+LAYOUT = pytest.mark.parametrize("page", [0, 64, 128, 512], ids=["buffers", "p64", "p128", "p512"])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from decode_attention_10_b200 import build, mfa
+    build.build()
+    mfa.load()
+
+
+def run(b, ws=None, **kw):
+    from decode_attention_10_b200 import mfa
+    ws = ws or mfa.ChunkWorkspace(b.batch)
+    cache = b.cache()
+    out = mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, ws=ws, **kw)
+    assert mfa.get_error(ws) == 0
+    return out
+
+
+@KV
+@LAYOUT
+@pytest.mark.parametrize("new,cached", [
+    ([1], [0]), ([1], [1]), ([2], [0]), ([3], [126]), ([4], [124]), ([4], [125]), ([5], [127]),
+    ([1], [127]), ([1], [128]), ([7], [60]), ([130], [0]), ([67], [301]), ([9], [2000]),
+])
+def test_one_sequence(fp8, page, new, cached):
+    b = Batch(new, cached, fp8, page, seed=sum(new) + sum(cached))
+    check(run(b), b)
+
+
+@KV
+@LAYOUT
+def test_ragged_batch_with_empty_sequences(fp8, page):
+    # decoding sequences, chunks of every remainder of 4, and sequences with no new token
+    new = [1, 0, 4, 33, 1, 0, 2, 65, 3, 1, 0]
+    cached = [500, 70, 128, 95, 0, 0, 1023, 7, 62, 129, 300]
+    b = Batch(new, cached, fp8, page, seed=3, spare=40)
+    check(run(b), b)
+
+
+@KV
+def test_long_context_is_split_and_joined(fp8):
+    b = Batch([3, 1], [20001, 9000], fp8, 64, seed=4)
+    check(run(b), b)
+
+
+@KV
+def test_chunk_over_a_long_context(fp8):
+    b = Batch([150], [5003], fp8, 128, seed=5)
+    check(run(b), b)
+
+
+@KV
+def test_many_sequences(fp8):
+    new = [(7 * i) % 5 for i in range(1024)]
+    cached = [(37 * i) % 300 for i in range(1024)]
+    b = Batch(new, cached, fp8, 64, seed=6)
+    check(run(b), b)
+
+
+@KV
+@LAYOUT
+def test_rows_past_the_end_are_never_weighted(fp8, page):
+    # NaN (and, in bf16, infinities) past every sequence's end, in its own pages and rows
+    for tail in (float("nan"),) if fp8 else (float("nan"), float("inf")):
+        b = Batch([5, 1, 4, 66], [123, 64, 0, 190], fp8, page, seed=7, spare=70, tail=tail)
+        out = run(b)
+        assert torch.isfinite(out).all()
+        check(out, b)
+
+
+@KV
+@LAYOUT
+@pytest.mark.parametrize("cached", [0, 61, 125, 126, 127, 200])
+def test_a_token_s_bad_rows_reach_it_and_later_tokens_only(fp8, page, cached):
+    # the K and V rows of new token 2 (of 7) hold NaN; the V row of token 5 an infinity
+    b = Batch([7], [cached], fp8, page, seed=8, spare=10)
+    clean = run(b)
+    nan = 0x7F if fp8 else 0x7FC0
+    for which in ("k", "v"):
+        set_row(b, which, 0, cached + 2, nan)
+    if not fp8:
+        set_row(b, "v", 0, cached + 5, 0x7F80)
+    out = run(b)
+    assert torch.equal(out[:2], clean[:2])
+    assert out[2:].isnan().all()
+    b = Batch([7], [cached], fp8, page, seed=8, spare=10)
+    set_row(b, "v", 0, cached + 5, nan, dims=slice(3, 4))  # one value of one row
+    out = run(b)
+    assert torch.equal(out[:5], clean[:5])
+    assert out[5:, :, 3].isnan().all()
+    out[5:, :, 3] = clean[5:, :, 3]  # its other values weigh as ever
+    check(out, Batch([7], [cached], fp8, page, seed=8, spare=10))
+
+
+def set_row(b, which, seq, row, bits, dims=slice(0, DIM)):
+    buf = b.k if which == "k" else b.v
+    t = buf if b.page else buf[seq]
+    raw = t.view(torch.uint8 if b.fp8 else torch.int16)
+    if b.page:
+        raw[int(b.table[seq, row // b.page]), row % b.page, dims] = bits
+    else:
+        raw[row, dims] = bits
+
+
+@KV
+def test_a_bad_query_reaches_its_own_row_only(fp8):
+    b = Batch([6], [100], fp8, 64, seed=9)
+    clean = run(b)
+    b.q[2, 17] = float("nan")
+    b.q[4, 3, 5] = float("inf")
+    out = run(b)
+    keep = torch.ones(6, HEADS, dtype=torch.bool)
+    keep[2, 17] = keep[4, 3] = False
+    assert torch.equal(out[keep], clean[keep])
+    assert out[2, 17].isnan().all()
+
+
+def test_scores_of_minus_infinity():
+    # keys of -inf in visible rows: weight zero next to finite ones, NaN where all are so
+    b = Batch([4], [300], False, 64, seed=10)
+    b.q.fill_(0.5)
+    for row in range(0, 256):
+        set_row(b, "k", 0, row, 0xFF80 - 0x10000)
+    out = run(b)
+    k, v = b.values("k", 0), b.values("v", 0)
+    for i in range(4):
+        s = (b.q[i].double() @ k[256:301 + i].T) / 16
+        want = torch.softmax(s, -1) @ v[256:301 + i]
+        mag = torch.softmax(s, -1) @ v[256:301 + i].abs()
+        assert ((out[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -7 * mag).all()
+    b = Batch([4], [3], False, 64, seed=10)
+    b.q.fill_(0.5)
+    for row in range(0, 5):
+        set_row(b, "k", 0, row, 0xFF80 - 0x10000)
+    out = run(b)
+    assert out[:2].isnan().all() and torch.isfinite(out[2:]).all()
+
+
+@KV
+@pytest.mark.parametrize("q_scale", [0.01, 8.0, 40.0])
+def test_flat_and_sharp_softmax(fp8, q_scale):
+    b = Batch([9, 70], [700, 450], fp8, 128, seed=11, q_scale=q_scale)
+    check(run(b), b)
+
+
+@KV
+def test_rising_scores_rescale_at_every_block(fp8):
+    # keys grow along the context, so every block raises the running maximum
+    b = Batch([5], [1200], fp8, 0, seed=12)
+    grow = torch.linspace(0.02, 1.0, b.total[0], device="cuda")[:, None]
+    u = torch.randn(DIM, generator=torch.Generator().manual_seed(1)).cuda()
+    rows = grow * u
+    b.k[0][:] = (rows / b.k_scale).clamp(-448, 448).to(b.k[0].dtype)
+    b.q[:] = (u + 0.1 * b.q.float()).to(torch.bfloat16)
+    check(run(b), b)
+
+
+@KV
+def test_rows_of_no_sequence_stay(fp8):
+    b = Batch([3, 6], [40, 200], fp8, 64, seed=13, lead=2, behind=9)
+    out = torch.full_like(b.q, 77.0)
+    run(b, out=out)
+    check(out, b)
+    assert (out[:2] == 77.0).all() and (out[b.starts[-1]:] == 77.0).all()
+
+
+@KV
+def test_scale_is_an_argument(fp8):
+    b = Batch([5], [333], fp8, 64, seed=14)
+    check(run(b, scale=0.17), b, scale=0.17)
+
+
+@KV
+def test_agrees_with_the_decode_attention(fp8):
+    # one new token a sequence is mfa_decode_attn
+    from decode_attention_10_b200 import mfa
+    b = Batch([1] * 9, [0, 5, 127, 128, 129, 700, 2047, 64, 63], fp8, 128, seed=15)
+    out = run(b)
+    ws = mfa.Workspace(b.batch)
+    ref = mfa.decode_attn(b.q, b.cache(), b.seq_lens, ws=ws)
+    check(out, b)
+    check(ref, b)
+    assert (out.float() - ref.float()).abs().max() <= 2e-2
+
+
+@KV
+def test_same_call_same_bits(fp8):
+    b = Batch([70, 1, 5, 1], [3000, 9000, 100, 0], fp8, 64, seed=16)
+    first = run(b)
+    for _ in range(3):
+        assert torch.equal(run(b), first)
+
+
+def test_errors_are_reported_and_zero_filled():
+    from decode_attention_10_b200 import mfa
+    b = Batch([2, 3, 4, 2], [50, 60, 0, 200], False, 64, seed=17)
+    ws = mfa.ChunkWorkspace(4)
+    cache = b.cache()
+    good = run(b)
+    bad = b.seq_lens.clone()
+    bad[1] = 129  # over the capacity of two pages
+    out = torch.full_like(b.q, 5.0)
+    mfa.chunk_attn(b.q, cache, b.q_start, bad, out=out, ws=ws)
+    assert mfa.get_error(ws) == 3 and mfa.get_error(ws) == 0
+    assert (out[2:5] == 0).all()
+    assert torch.equal(out[:2], good[:2]) and torch.equal(out[5:], good[5:])
+    for length in (3, 0, -7):  # fewer positions than new tokens
+        bad = b.seq_lens.clone()
+        bad[2] = length
+        out = torch.full_like(b.q, 5.0)
+        mfa.chunk_attn(b.q, cache, b.q_start, bad, out=out, ws=ws)
+        assert mfa.get_error(ws) == 6
+        assert (out[5:9] == 0).all()
+        assert torch.equal(out[:5], good[:5]) and torch.equal(out[9:], good[9:])
+    # ranges outside the rows: not computed, nothing written outside `out`
+    for starts in ([0, 2, 5, 9, 40], [-3, 2, 5, 9, 11], [0, 2, 1, 4, 11], [0, 2, 5, 900, 11]):
+        out = torch.full_like(b.q, 5.0)
+        q_start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        mfa.chunk_attn(b.q, cache, q_start, b.seq_lens, out=out, ws=ws)
+        assert mfa.get_error(ws) == 1
+    out = torch.full_like(b.q, 5.0)
+    mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, out=out, ws=ws)
+    assert mfa.get_error(ws) == 0 and torch.equal(out, good)
+
+
+def test_table_without_chunk_maps_is_refused():
+    from decode_attention_10_b200 import mfa
+    import ctypes
+    b = Batch([2], [50], False, 0, seed=18)
+    lib = mfa.load()
+    small = lib.mfa_kv_table_bytes(1)
+    table = torch.zeros(small + 512, dtype=torch.uint8, device="cuda")
+    arr = (ctypes.c_void_p * 1)(b.k[0].data_ptr())
+    arv = (ctypes.c_void_p * 1)(b.v[0].data_ptr())
+    cap = (ctypes.c_int32 * 1)(b.cap[0])
+    assert lib.mfa_kv_table_init(table.data_ptr(), small, 1, 0, arr, arv, cap, None) == 0
+    assert (table[small:] == 0).all()
+    cache = b.cache()
+    cache.desc.table = table.data_ptr()
+    ws = mfa.ChunkWorkspace(1)
+    out = torch.full_like(b.q, 5.0)
+    mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, out=out, ws=ws)
+    assert mfa.get_error(ws) == 1 and (out == 5.0).all()
+    # a stated layout that the table contradicts
+    cache = b.cache()
+    cache.desc.page_size = 64
+    mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, out=out, ws=ws)
+    assert mfa.get_error(ws) == 1 and (out == 5.0).all()
+
+
+def test_page_outside_the_pool_reads_as_zeros():
+    # as in mfa_decode_attn: such a page's keys and values are zeros
+    b = Batch([3], [300], False, 64, seed=19)
+    ref = run(b)
+    b.table[0, 1] = 10 ** 6
+    out = run(b)
+    assert torch.isfinite(out).all() and not torch.equal(out, ref)
+    b.table[0, 1] = -1
+    assert torch.equal(run(b), out)
+
+
+@KV
+def test_captured_and_replayed(fp8):
+    # replays read the lengths, starts and pages of their time
+    from decode_attention_10_b200 import mfa
+    a = Batch([4, 1, 20], [100, 700, 0], fp8, 64, seed=20, spare=500)
+    ws = mfa.ChunkWorkspace(3)
+    cache = a.cache()
+    out = torch.zeros_like(a.q)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        mfa.chunk_attn(a.q, cache, a.q_start, a.seq_lens, out=out, ws=ws)
+    torch.cuda.synchronize()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        mfa.chunk_attn(a.q, cache, a.q_start, a.seq_lens, out=out, ws=ws)
+        mfa.chunk_attn(a.q, cache, a.q_start, a.seq_lens, out=out, ws=ws)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    a.q_start.copy_(torch.tensor([0, 1, 5, 25], dtype=torch.int32))
+    a.seq_lens.copy_(torch.tensor([101, 704, 20], dtype=torch.int32))
+    a.q.copy_(torch.randn_like(a.q.float()).to(torch.bfloat16))
+    fresh = mfa.chunk_attn(a.q, cache, a.q_start, a.seq_lens)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, fresh) and mfa.get_error(ws) == 0
+
+
+def test_two_calls_on_two_streams_with_workspaces_of_their_own():
+    from decode_attention_10_b200 import mfa
+    bs = [Batch([50, 3], [2000, 4000], False, 64, seed=21), Batch([7], [6000], True, 0, seed=22)]
+    caches = [b.cache() for b in bs]
+    wss = [mfa.ChunkWorkspace(b.batch) for b in bs]
+    want = [run(b) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    outs = [torch.zeros_like(b.q) for b in bs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, c, w, s, o in zip(bs, caches, wss, streams, outs):
+            mfa.chunk_attn(b.q, c, b.q_start, b.seq_lens, out=o, ws=w, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
