@@ -649,7 +649,14 @@ mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* 
   a.out = static_cast<uint16_t*>(out);
   a.partials = at<float>(ws, L.total);
   a.err = at<uint32_t>(ws, L.err);
-  return cuda_status(launch_chunk_attn(a, static_cast<cudaStream_t>(stream)));
+  const int slots = chunk_grid_for(sms);
+  a.info = reinterpret_cast<int2*>(a.partials + 2 * (size_t)slots * kChunkPartialFloats);
+  const int resident = chunk_attn_pairs(a);
+  if (resident <= 0) return MFA_ERR_CUDA;
+  a.pairs = resident < slots ? resident : slots;
+  CUtensorMap q_map;
+  if (!encode_2d(&q_map, q, (uint64_t)n_rows * kHeads, kHeadDim, 2, 64, 128)) return MFA_ERR_CUDA;
+  return cuda_status(launch_chunk_attn(q_map, a, static_cast<cudaStream_t>(stream)));
 }
 
 mfa_status mfa_o_proj(const void* out, const void* w_o, void* y, int32_t batch, void* ws,

@@ -1,11 +1,50 @@
 // Causal attention of a chunk of new tokens over the KV cache (include/mfa.h:
-// mfa_chunk_attn).
+// mfa_chunk_attn), on the sm_100a tensor cores, for bf16 and FP8 (e4m3) caches:
+//     out[t][h] = sum_{j <= p_t} softmax_j(scale q[t][h] . K[j]) V[j],  p_t the token's position.
 //
-// out[t][h] = sum_{j <= p_t} softmax_j(scale q[t][h] . K[j]) V[j], with the running maximum
-// and sum of the softmax in float32. One warp per (token, head): a lane holds eight of the
-// 256 dimensions, every key costs one warp-wide sum.
+// All 64 heads share K and V, so the rows of q ([token][head], 256 dimensions) of consecutive
+// tokens form one tall matrix against the same keys. A tile is 4 tokens = 256 rows, worked on
+// by a pair of CTAs on two neighbouring SMs (tcgen05 cta_group::2, M = 256: 128 rows a CTA).
+// Per block of 128 keys
+//     S[256 x 128] = Q[256 x 256] . K^T          O[256 x 256] += P[256 x 128] . V
+// Each CTA loads half of K (64 keys) and half of V (128 of the 256 dimensions); the tensor
+// cores of both read both halves, so a pair streams 128 KB (bf16) per block for 256 rows: 32
+// bytes per SM and cycle at full tensor rate, half of what one CTA by itself would need from
+// L2. A pair keeps up with HBM even when one token a sequence leaves 3/4 of its rows idle
+// (a block takes the tensor cores 2048 cycles, and 1/74 of the measured bandwidth ~2800), so
+// the same kernel serves decoding and prompts.
+//
+// Tensor memory (512 columns): O in 256, two S buffers of 128. P overwrites its own S (16-bit:
+// the first 64 of the 128 columns) and is read by the product as the tensor-memory operand, so
+// it never passes through shared memory. Shared memory: Q 64 KB, and a ring of nine 16 KB
+// slots for K and V halves. Warps:
+//   warp 0      TMA producer of this CTA's halves (rows of 64 keys a box, 128-byte swizzle)
+//   warp 1      in the pair's first CTA: issues the products of both (one elected lane), in
+//               the order S(t + 1), O += P(t) V(t), so that S(t + 1) runs during the softmax
+//               of t; owns the tensor memory
+//   warps 2..9  softmax: two threads per row, 64 of the 128 keys each. Scores stay raw; a
+//               row's running maximum is raised only when a block exceeds it by more than 8
+//               in log2 (4 for FP8), so O is rarely rescaled; the pair of warps that shares 32
+//               rows agrees on that with one barrier a block. Sums in float32, of the
+//               unrounded weights.
+// FP8 caches: the codes go to the tensor cores as they are (kind::f8f6f4). Q and P become
+// pairs of e4m3 matrices, high part and rounded remainder, both accumulated into the same S
+// or O: twice the products at twice the rate, and half the bytes of K and V. Q's scale is a
+// power of two per row. P is kept below 2^8 by adding 4 to its exponent.
+//
+// Work split: tiles of all sequences laid end to end, each costing its blocks plus
+// kTileCost; pair g takes the g-th of G equal contiguous ranges, so causal chunks, prompts
+// and decoding sequences balance to within a block whatever the mix. A range that starts or
+// ends inside a tile leaves (m, l, O) partials in one of the pair's two slots, merged in a
+// fixed order by chunk_combine_kernel.
+//
+// Blocks that hold keys some token of the tile does not see are "special": at most the last
+// two of a tile. Their scores are masked by selection, so nothing a hidden key holds reaches a
+// weight; and as 0 x NaN is NaN, V rows past the tile's last position are zeroed on chip, and
+// rows that only its later tokens see are zeroed if they hold an infinity or NaN and then
+// added in float32 for the tokens that do see them.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "mfa_internal.cuh"
 #include "sm100.cuh"
@@ -13,103 +52,1187 @@
 namespace mfa {
 namespace {
 
+using namespace sm100;
+
+constexpr int kTokens = kChunkRows / kHeads;  // 4 tokens a tile
+constexpr int kRows = 128;                    // rows of a CTA (tensor-memory lanes)
+constexpr int kCtaTokens = kRows / kHeads;    // 2
+constexpr int kBlock = 128;                   // keys of a block
+constexpr int kSlotBytes = 16384;
+constexpr int kSlots = 9;
+constexpr int kBoxBytes = kChunkBoxRows * 128;  // [64 rows x 128 bytes]
+constexpr int kQChunkBytes = kRows * 128;       // [128 rows x 128 bytes]
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 64 + 32 * kSoftmaxWarps;
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
+constexpr int kTileCost = 1;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void load8(const KvSeq& s, const void* base, int dtype, long long at,
-                                      int lane, float (&f)[8]) {
-  if (dtype == MFA_KV_BF16) {
-    const uint4 v =
-        *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at * kHeadDim + 8 * lane);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    const uint2 v =
-        *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + at * kHeadDim + 8 * lane);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = i < 4 ? v.x : v.y;
-      __nv_fp8_e4m3 x;
-      x.__x = static_cast<__nv_fp8_storage_t>(w >> (8 * (i % 4)));
-      f[i] = static_cast<float>(x);
+template <bool kFp8>
+struct Cfg {
+  static constexpr int kKSlots = kFp8 ? 1 : 2;  // ring slots of a CTA's half of a K block
+  static constexpr int kVSlots = kFp8 ? 1 : 2;
+  static constexpr float kRescale = kFp8 ? 4.0f : 8.0f;  // log2 units
+  static constexpr float kPExp = kFp8 ? 4.0f : 0.0f;     // P = 2^(s - m + kPExp)
+  static constexpr uint32_t kIdescS = idesc_f16(256, kBlock, !kFp8, false, false);
+  static constexpr uint32_t kIdescPV = idesc_f16(256, kHeadDim, !kFp8, false, true);
+};
+
+struct Plan {
+  int32_t cost[kMaxBatch + 1];   // exclusive prefix of the sequences' costs
+  int32_t start[kMaxBatch + 1];  // q_start
+  int32_t len[kMaxBatch];        // seq_lens; -1: refused
+};
+
+struct __align__(1024) Smem {
+  uint8_t q[4 * kQChunkBytes];
+  uint8_t ring[kSlots * kSlotBytes];
+  Plan plan;
+  float xch[2][kRows];        // exchange between the two threads of a row
+  uint64_t kv_full[kSlots];   // first CTA: both halves of a slot have landed
+  uint64_t kv_empty[kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2];
+  uint64_t v_full[kSlots];    // this CTA: a slot's V half of a special block has landed
+  uint64_t pv_done[2];        // by the block's parity: a waiter is at most one block behind
+  uint64_t o_free;
+  uint64_t mma_done;
+  uint32_t bad[2][2];         // [item parity][V half]: late rows held out of the product
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory per CTA");
+
+// ---------------------------------------------------------------------------------------
+// pair (cluster of two CTAs) primitives
+// ---------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// shared::cluster address of this CTA's `p` in CTA `rank` of the pair
+__device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void remote_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// As mbar_wait, for arrivals that come from the other CTA too.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
+                                             volatile int* abort) {
+  if (*abort) return false;
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        return false;
+      }
     }
   }
 }
 
-__global__ void __launch_bounds__(256) chunk_attn_kernel(ChunkAttnArgs a) {
-  sm100::pdl_launch_dependents();
-  sm100::pdl_wait();
-  const int row = blockIdx.x, lane = threadIdx.x & 31;
-  const int head = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (row == 0 && head < 8) {
-    for (int b = threadIdx.x; b < a.batch; b += 256) {
-      const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
-      if (s0 < 0 || s1 < s0 || s1 > a.n_rows) atomicOr(a.err, kErrLayout);
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+// TMA loads into this CTA that complete on a barrier of either CTA of the pair.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, int x, int y,
+                                             uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, int x, int y,
+                                             int z, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst_smem)),
+               "n"(kTmemCols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr),
+               "n"(kTmemCols)
+               : "memory");
+}
+
+// Arrive on `bar` of both CTAs when every tcgen05 operation issued so far is done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n"
+      ".reg .b16 m;\n"
+      "mov.b16 m, 3;\n"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], m;\n"
+      "}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A . B over the pair; A in shared memory (SS) or tensor memory (TS).
+template <bool kFp8>
+__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                            uint32_t acc) {
+  if constexpr (kFp8)
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+  else
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+}
+template <bool kFp8>
+__device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc,
+                                            uint32_t acc) {
+  if constexpr (kFp8)
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+  else
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+}
+
+// ---------------------------------------------------------------------------------------
+// the work split
+// ---------------------------------------------------------------------------------------
+
+// sum_{i = 1}^{m} ceil((p + 4 i) / 128): with a = p + 127 = 4 c + r, floor((a + 4 i) / 128) =
+// floor((c + i) / 32), so it is a difference of G(x) = sum_{j <= x} floor(j / 32).
+__device__ __forceinline__ int block_sum(int p, int m) {
+  auto G = [](int x) {
+    const int q = x >> 5;
+    return 16 * q * (q - 1) + q * ((x & 31) + 1);
+  };
+  const int c = (p + kBlock - 1) >> 2;
+  return G(c + m) - G(c);
+}
+
+// Cost of the tiles before tile m of a sequence whose chunk starts at position p.
+__device__ __forceinline__ int tile_offset(int p, int m) { return m * kTileCost + block_sum(p, m); }
+
+// Cost of n new tokens that end at position len (all their tiles; the last may be short).
+__device__ __forceinline__ int seq_cost(int n, int len) {
+  const int tiles = (n + kTokens - 1) / kTokens;
+  return tile_offset(len - n, tiles - 1) + kTileCost + (len + kBlock - 1) / kBlock;
+}
+static_assert(kTokens == 4 && kBlock == 128, "block_sum's closed form");
+
+// Range g of G nearly equal ones of [0, total), and the range that holds unit t. (total is
+// below 2^30: at most 2^20 + 2^10 tiles of at most 513 + kTileCost units.)
+__device__ __forceinline__ int range_begin(int g, int G, int total) {
+  return g * (total / G) + min(g, total % G);
+}
+__device__ __forceinline__ int range_of(int t, int G, int total) {
+  const int q = total / G, r = total % G, cut = r * (q + 1);
+  return t < cut ? t / (q + 1) : r + (t - cut) / q;
+}
+static_assert((MFA_MAX_ROWS / kTokens + kMaxBatch) * (int64_t)(MFA_MAX_CONTEXT / kBlock + 1 + kTileCost) <
+                  (1ll << 30),
+              "costs fit 32 bits");
+
+struct Item {
+  int b;          // sequence
+  int row0;       // first token's row of q
+  int ntok;       // tokens of the tile, 1 .. 4
+  int p0;         // position of the first
+  int blk0, blk1; // blocks of this item
+  int nblk;       // blocks of the tile
+  int cost0;      // the tile's first unit
+  __device__ int kend() const { return p0 + ntok; }          // one past the last key seen
+  __device__ int special() const { return (p0 + 1) / kBlock; }  // first special block
+  __device__ bool whole() const { return blk0 == 0 && blk1 == nblk; }
+};
+
+struct Cursor {
+  const Plan* P;
+  int batch, begin, end, pos, b, tile;
+
+  __device__ void init(const Plan& plan, int batch_, int g, int G) {
+    P = &plan;
+    batch = batch_;
+    const int total = plan.cost[batch];
+    begin = end = pos = b = tile = 0;
+    if (total == 0 || g >= G) return;
+    begin = range_begin(g, G, total);
+    end = range_begin(g + 1, G, total);
+    // the sequence, then the tile, that hold unit `begin`
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan.cost[mid] <= begin) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    const int n = plan.start[b + 1] - plan.start[b], p = plan.len[b] - n;
+    int t0 = 0, t1 = (n + kTokens - 1) / kTokens - 1;
+    while (t0 < t1) {
+      const int mid = (t0 + t1 + 1) >> 1;
+      if (plan.cost[b] + tile_offset(p, mid) <= begin) t0 = mid; else t1 = mid - 1;
+    }
+    tile = t0;
+    pos = plan.cost[b] + tile_offset(p, tile);
+  }
+
+  __device__ bool next(Item& it) {
+    while (pos < end) {
+      const int n = P->start[b + 1] - P->start[b];
+      it.b = b;
+      it.ntok = min(kTokens, n - kTokens * tile);
+      it.row0 = P->start[b] + kTokens * tile;
+      it.p0 = P->len[b] - n + kTokens * tile;
+      it.nblk = (it.kend() + kBlock - 1) / kBlock;
+      it.cost0 = pos;
+      it.blk0 = max(0, begin - pos - kTileCost);
+      it.blk1 = min(it.nblk, end - pos - kTileCost);
+      pos += kTileCost + it.nblk;
+      ++tile;
+      if (kTokens * tile >= n) {
+        tile = 0;
+        do ++b; while (b < batch && P->cost[b + 1] == P->cost[b]);
+      }
+      if (it.blk1 > it.blk0) return true;
+    }
+    return false;
+  }
+};
+
+// Every thread of the CTA: the sequences' costs, from the lengths on the device. Refused
+// sequences cost nothing (len -1) and, if `report`, are flagged.
+__device__ void build_plan(Smem& S, const ChunkAttnArgs& a, bool report) {
+  Plan& P = S.plan;
+  uint32_t bits = 0;
+  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], L = a.seq_lens[b];
+    const KvSeq& kv = a.kv[b];
+    int cost = 0, len = L;
+    if (kv.chunk_maps == 0 || kv.page_size != a.page_size) {
+      bits |= kErrLayout;
+      len = -2;  // nothing at all is computed
+    } else if (s0 < 0 || s1 < s0 || s1 > a.n_rows) {
+      bits |= kErrLayout;
+      len = -2;  // no rows to speak of
+    } else if (s1 > s0) {
+      if (L > kv.capacity) {
+        bits |= kErrCapacity;
+        len = -1;
+      } else if (L < s1 - s0) {
+        bits |= kErrEmpty;
+        len = -1;
+      } else {
+        cost = seq_cost(s1 - s0, L);
+      }
+    }
+    P.start[b] = s0;
+    P.len[b] = len;
+    P.cost[b] = cost;
+    if (b == a.batch - 1) P.start[a.batch] = s1;
+  }
+  if (report && bits != 0) atomicOr(a.err, bits);
+  __syncthreads();
+  // exclusive prefix: warp 0, each lane a run of sequences
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (a.batch + 31) / 32;
+    const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += P.cost[b];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int run = incl - sum;
+    for (int b = b0; b < b1; ++b) {
+      const int c = P.cost[b];
+      P.cost[b] = run;
+      run += c;
+    }
+    if (lane == 31) P.cost[a.batch] = incl;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float* slot_m(float* base, int slot) {
+  return base + slot * kChunkPartialFloats;
+}
+__device__ __forceinline__ float* slot_l(float* base, int slot) {
+  return base + slot * kChunkPartialFloats + kChunkRows;
+}
+__device__ __forceinline__ float* slot_acc(float* base, int slot) {
+  return base + slot * kChunkPartialFloats + 2 * kChunkRows;
+}
+
+// ---------------------------------------------------------------------------------------
+// warp 0: TMA producer
+// ---------------------------------------------------------------------------------------
+
+// The page ids of a sequence's 64-row groups, 32 ahead in a register of each lane and the
+// next 32 on their way, so that no copy waits for the page table.
+struct Groups {
+  const int32_t* pages;
+  int base, last, shift;  // shift: log2(rows of a page) - 6
+  int now, ahead;
+  __device__ int fetch(int g0, int lane) const {
+    const int g = g0 + lane;
+    return g <= last ? pages[g >> shift] : 0;
+  }
+  __device__ void init(const KvSeq& s, int g0, int last_, int shift_, int lane) {
+    pages = s.pages;
+    last = last_;
+    shift = shift_;
+    base = g0;
+    now = fetch(base, lane);
+    ahead = fetch(base + 32, lane);
+  }
+  __device__ int page(int g, int lane) {
+    if (g >= base + 32) {
+      base += 32;
+      now = ahead;
+      ahead = fetch(base + 32, lane);
+    }
+    return __shfl_sync(0xffffffffu, now, g - base);
+  }
+};
+
+template <bool kFp8, bool kPaged>
+__device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnArgs& a, int g,
+                             int G, uint32_t rank) {
+  using C = Cfg<kFp8>;
+  volatile int* abort = &S.abort_flag;
+  const int lane = threadIdx.x & 31;
+  const bool leader = lane == 0;
+  const KvChunkMaps* maps = reinterpret_cast<const KvChunkMaps*>(a.kv + a.batch);
+  const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
+  const uint32_t q_bar = map_to(&S.q_full, 0);
+  const int page_shift = kPaged ? 31 - __clz(a.page_size) : 0;
+  uint32_t chunk = 0, issued = 0;
+  int item = 0;
+  Cursor cur;
+  cur.init(S.plan, a.batch, g, G);
+  Item it;
+  while (cur.next(it)) {
+    const KvChunkMaps* map = maps + it.b;
+    if (leader) {
+      prefetch_tensormap(&map->k);
+      prefetch_tensormap(&map->v);
+    }
+    if constexpr (!kFp8) {
+      if (item > 0) mbar_wait(&S.q_empty, (item - 1) & 1, abort);
+      if (leader && !*abort) {
+        if (rank == 0) mbar_arrive_expect_tx(&S.q_full, 2 * 4 * kQChunkBytes);
+        const int y = (it.row0 + kCtaTokens * rank) * kHeads;
+        for (int c = 0; c < 4; ++c)
+          pair_load_2d(S.q + c * kQChunkBytes, q_map, 64 * c, y, q_bar, once);
+      }
+    }
+    // one tile of the sequence reads its rows once; several find them in L2
+    const uint64_t policy =
+        S.plan.start[it.b + 1] - S.plan.start[it.b] <= kTokens ? once : keep;
+    const int last_group = (it.kend() - 1) / kChunkBoxRows;
+    Groups kg, vg;
+    if constexpr (kPaged) {
+      kg.init(a.kv[it.b], 2 * it.blk0, last_group, page_shift - 6, lane);
+      vg = kg;
+    }
+    // 64 rows from group gr on, `boxes` boxes of 128 bytes a row from column x on
+    auto load = [&](uint8_t* dst, const CUtensorMap* m, Groups& groups, int gr, int x,
+                    int boxes, uint32_t bar) {
+      int page = 0, y = gr * kChunkBoxRows;
+      if constexpr (kPaged) {
+        page = groups.page(gr, lane);
+        // groups past the last key: rows outside the page, which read as zeros
+        y = gr <= last_group ? y & (a.page_size - 1) : a.page_size;
+      }
+      if (leader && !*abort) {
+        for (int i = 0; i < boxes; ++i) {
+          const int xx = x + i * (kFp8 ? 128 : 64);
+          if constexpr (kPaged)
+            pair_load_3d(dst + i * kBoxBytes, m, xx, y, page, bar, policy);
+          else
+            pair_load_2d(dst + i * kBoxBytes, m, xx, y, bar, policy);
+        }
+      }
+    };
+    // the next slot of the ring, free, and the barrier that its bytes complete on: the pair's,
+    // or (local) this CTA's. Both barriers see a phase per use of the slot.
+    auto take = [&](bool local, uint32_t& bar) {
+      const uint32_t slot = chunk % kSlots, use = chunk / kSlots;
+      if (use > 0) mbar_wait(&S.kv_empty[slot], (use - 1) & 1, abort);
+      if (leader && !*abort) {
+        if (local) {
+          mbar_arrive_expect_tx(&S.v_full[slot], kSlotBytes);
+          if (rank == 0) mbar_arrive(&S.kv_full[slot]);
+        } else {
+          mbar_arrive(&S.v_full[slot]);
+          if (rank == 0) mbar_arrive_expect_tx(&S.kv_full[slot], 2 * kSlotBytes);
+        }
+        issued = chunk + 1;
+      }
+      bar = local ? smem_u32(&S.v_full[slot]) : map_to(&S.kv_full[slot], 0);
+      ++chunk;
+      return S.ring + slot * kSlotBytes;
+    };
+    auto load_k = [&](int blk) {
+      uint32_t bar;
+      // this CTA's 64 keys, all dimensions
+      for (int c = 0; c < C::kKSlots; ++c) {
+        uint8_t* dst = take(false, bar);
+        load(dst, &map->k, kg, 2 * blk + rank, c * 128, 2, bar);
+      }
+    };
+    auto load_v = [&](int blk) {
+      // all keys, this CTA's 128 dimensions. Special blocks land on this CTA's own barrier:
+      // its softmax warps look them over before the product may read them.
+      const bool local = blk >= it.special();
+      const int x = 128 * rank;
+      uint32_t bar;
+      for (int c = 0; c < C::kVSlots; ++c) {
+        uint8_t* dst = take(local, bar);
+        if constexpr (kFp8) {
+          load(dst, &map->v, vg, 2 * blk, x, 1, bar);
+          load(dst + kBoxBytes, &map->v, vg, 2 * blk + 1, x, 1, bar);
+        } else {
+          load(dst, &map->v, vg, 2 * blk + c, x, 2, bar);
+        }
+      }
+    };
+    load_k(it.blk0);
+    for (int blk = it.blk0; blk < it.blk1; ++blk) {
+      if (blk + 1 < it.blk1) load_k(blk + 1);
+      load_v(blk);
+    }
+    ++item;
+  }
+  // Before the CTAs may exit, every copy must have landed (after an abort; else all were used).
+  if (*abort && leader) {
+    for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c) {
+      if (rank == 0) mbar_wait_drain(&S.kv_full[c % kSlots], (c / kSlots) & 1);
+      mbar_wait_drain(&S.v_full[c % kSlots], (c / kSlots) & 1);
+    }
+    if (!kFp8 && rank == 0 && item > 0) mbar_wait_drain(&S.q_full, (item - 1) & 1);
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------------------
+// warp 1 of the first CTA: the products
+// ---------------------------------------------------------------------------------------
+template <bool kFp8>
+__device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t tmem) {
+  using C = Cfg<kFp8>;
+  volatile int* abort = &S.abort_flag;
+  const bool leader = (threadIdx.x & 31) == 0;
+  uint32_t chunk = 0, gt = 0;
+  int item = 0;
+  const uint32_t q_base = smem_u32(S.q), ring = smem_u32(S.ring);
+
+  auto issue_s = [&](uint32_t t) {
+    const uint32_t d = tmem + kTmemS + kBlock * (t & 1);
+#pragma unroll
+    for (int c = 0; c < C::kKSlots; ++c, ++chunk) {
+      const uint32_t slot = chunk % kSlots;
+      wait_cluster(&S.kv_full[slot], (chunk / kSlots) & 1, abort);
+      tc_fence_after();
+      if (leader && !*abort) {
+        const uint32_t kb = ring + slot * kSlotBytes;
+        if constexpr (kFp8) {
+          // high parts, then low parts of Q, over the same keys
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int part = i >> 3, box = (i >> 2) & 1, kk = i & 3;
+            pair_mma_ss<true>(
+                d, sdesc_sw128(q_base + (2 * part + box) * kQChunkBytes + 32 * kk, 16, 1024),
+                sdesc_sw128(kb + box * kBoxBytes + 32 * kk, 16, 1024), C::kIdescS, i != 0);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int box = i >> 2, kk = i & 3;
+            pair_mma_ss<false>(
+                d, sdesc_sw128(q_base + (2 * c + box) * kQChunkBytes + 32 * kk, 16, 1024),
+                sdesc_sw128(kb + box * kBoxBytes + 32 * kk, 16, 1024), C::kIdescS,
+                (c | i) != 0);
+          }
+        }
+        pair_commit(&S.kv_empty[slot]);
+      }
+    }
+    if (leader && !*abort) pair_commit(&S.s_full[t & 1]);
+  };
+
+  auto issue_pv = [&](uint32_t t, bool first) {
+    wait_cluster(&S.p_full[t & 1], (t >> 1) & 1, abort);
+    if (first && item > 0) wait_cluster(&S.o_free, (item - 1) & 1, abort);
+    tc_fence_after();
+    const uint32_t d = tmem + kTmemO, p = tmem + kTmemS + kBlock * (t & 1);
+#pragma unroll
+    for (int c = 0; c < C::kVSlots; ++c, ++chunk) {
+      const uint32_t slot = chunk % kSlots;
+      wait_cluster(&S.kv_full[slot], (chunk / kSlots) & 1, abort);
+      tc_fence_after();
+      if (leader && !*abort) {
+        const uint32_t vb = ring + slot * kSlotBytes;
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int part = i >> 2, kt = i & 3;  // 32 keys each
+            pair_mma_ts<true>(d, p + 32 * part + 8 * kt, sdesc_sw128(vb + 4096 * kt, kBoxBytes, 1024),
+                              C::kIdescPV, !(first && i == 0));
+          }
+        } else {
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt)  // 16 keys each
+            pair_mma_ts<false>(d, p + 8 * (4 * c + kt), sdesc_sw128(vb + 2048 * kt, kBoxBytes, 1024),
+                               C::kIdescPV, !(first && c == 0 && kt == 0));
+        }
+        pair_commit(&S.kv_empty[slot]);
+      }
+    }
+    if (leader && !*abort) pair_commit(&S.pv_done[t & 1]);
+  };
+
+  Cursor cur;
+  cur.init(S.plan, a.batch, g, G);
+  Item it;
+  while (cur.next(it)) {
+    const int n = it.blk1 - it.blk0;
+    wait_cluster(&S.q_full, item & 1, abort);
+    tc_fence_after();
+    issue_s(gt);
+    for (int t = 0; t < n; ++t) {
+      if (t + 1 < n) issue_s(gt + t + 1);
+      if (t + 1 == n && !kFp8 && leader && !*abort) pair_commit(&S.q_empty);
+      issue_pv(gt + t, t == 0);
+    }
+    gt += n;
+    ++item;
+  }
+  // every product must be done before the tensor memory is released
+  if (leader) pair_commit(&S.mma_done);
+  mbar_wait_drain(&S.mma_done, 0);
+}
+
+// ---------------------------------------------------------------------------------------
+// warps 2..9: softmax, rescale, epilogue
+// ---------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// f16x2 as e4m3 high and low parts: hi = e4m3(v), lo = e4m3(v - hi) (exact difference)
+__device__ __forceinline__ void split_e4m3x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  uint32_t back, rest;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(v));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(v), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(rest));
+  hi = h;
+  lo = l;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Eight consecutive values of a cache row (element offset `at`), as float32.
+template <bool kFp8>
+__device__ __forceinline__ void load8(const void* base, long long at, float (&f)[8]) {
+  if constexpr (kFp8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + at);
+    const uint16_t h[4] = {static_cast<uint16_t>(v.x), static_cast<uint16_t>(v.x >> 16),
+                           static_cast<uint16_t>(v.y), static_cast<uint16_t>(v.y >> 16)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(h[i]));
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    }
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
     }
   }
-  int seq = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 256)
-    seq += __syncthreads_count(b0 + threadIdx.x < a.batch &&
-                               a.q_start[b0 + threadIdx.x + 1] <= row);
-  if (seq >= a.batch || row < a.q_start[seq]) return;
-  const KvSeq& s = a.kv[seq];
-  if (s.page_size != a.page_size || s.chunk_maps == 0) {
-    if (threadIdx.x == 0) atomicOr(a.err, kErrLayout);
-    return;
+}
+
+// FP8: this thread's 128 dimensions of its row of Q, split into e4m3 high and low parts scaled
+// by 2^-e with the row's largest magnitude in [128, 256). Returns e. (bf16 times a power of
+// two is exact in f16 down to 2^-24 of 256; smaller elements round there.) The Q buffer must
+// be free: every S of the previous item has completed.
+__device__ __noinline__ int split_q(Smem& S, const ChunkAttnArgs& a, const Item& it, int rank,
+                                    int row, int half, uint32_t bar_id) {
+  const int tok = it.row0 + kCtaTokens * rank + row / kHeads;
+  const bool real = tok < a.n_rows;  // (a tile's missing tokens take whatever row is there)
+  const uint4* src = reinterpret_cast<const uint4*>(
+      a.q + (static_cast<size_t>(tok) * kHeads + row % kHeads) * kHeadDim + 128 * half);
+  uint4 v[16];
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
   }
-  const int n = a.q_start[seq + 1] - a.q_start[seq], L = a.seq_lens[seq];
-  const size_t o_at = (static_cast<size_t>(row) * kHeads + head) * kHeadDim + 8 * lane;
-  const uint32_t bits = a.q_start[seq + 1] > a.n_rows || a.q_start[seq] < 0 ? kErrLayout
-                        : L > s.capacity              ? kErrCapacity
-                        : L < n                       ? kErrEmpty
-                                                      : 0u;
-  if (bits != 0) {
-    if (threadIdx.x == 0) atomicOr(a.err, bits);
-    *reinterpret_cast<uint4*>(a.out + o_at) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int last = L - (a.q_start[seq + 1] - row);
-  float q[8], o[8], m = -INFINITY, l = 0.f;
-  {
-    KvSeq none{};
-    load8(none, a.q, MFA_KV_BF16, static_cast<long long>(row) * kHeads + head, lane, q);
-  }
-  const bool fp8 = a.kv_dtype == MFA_KV_FP8_E4M3;
-  const float mul = a.scale * kLog2e * (fp8 ? a.k_scale : 1.f);
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int j = 0; j <= last; ++j) {
-    const long long at = kv_row_index(s, j);
-    float k[8] = {}, v[8] = {};
-    if (at >= 0) {
-      load8(s, s.k, a.kv_dtype, at, lane, k);
-      load8(s, s.v, a.kv_dtype, at, lane, v);
+  S.xch[half][row] = mx;
+  named_bar_sync(bar_id, 64);
+  mx = fmaxf(mx, S.xch[half ^ 1][row]);
+  named_bar_sync(bar_id, 64);
+  // e >= -100 keeps 2^-e finite; a row with an infinity (its scores are NaN anyhow) takes 0
+  const int e = mx > 0.f && mx <= 3.0e38f ? max(ilogbf(mx) - 7, -100) : 0;
+  const float sc = ldexpf(1.f, -e);
+  uint8_t* hi_row = S.q + half * kQChunkBytes + row * 128;
+  uint8_t* lo_row = hi_row + 2 * kQChunkBytes;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {  // 16 dimensions a piece
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 x = v[2 * p + k / 2];
+      const uint32_t w0 = k % 2 ? x.z : x.x, w1 = k % 2 ? x.w : x.y;
+      uint32_t h0, l0, h1, l1;
+      split_e4m3x2(pack_f16x2(bf16_lo(w0) * sc, bf16_hi(w0) * sc), h0, l0);
+      split_e4m3x2(pack_f16x2(bf16_lo(w1) * sc, bf16_hi(w1) * sc), h1, l1);
+      hi[k] = h0 | (h1 << 16);
+      lo[k] = l0 | (l1 << 16);
     }
-    float x = 0.f;
-    for (int i = 0; i < 8; ++i) x = fmaf(q[i], k[i], x);
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= mul;
-    const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.f : mn;
-    const float w = exp2f(x - base), al = exp2f(m - base);
-    l = fmaf(l, al, w);
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(o[i], al, w * v[i]);
-    m = mn;
+    *reinterpret_cast<uint4*>(hi_row + ((p ^ (row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(lo_row + ((p ^ (row & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
-  const float r = (fp8 ? a.v_scale : 1.f) / l;
-  uint32_t w[4];
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i] * r, o[2 * i + 1] * r);
-    w[i] = *reinterpret_cast<uint32_t*>(&h);
+  return e;
+}
+
+// A special block's V half in this CTA's ring, by the 256 softmax threads (st): rows of keys
+// that no token of the tile sees are zeroed; by warp 0 of them, rows that only its later
+// tokens see (key p0 + 1 + i, i < ntok - 1) are zeroed too if they hold an infinity or NaN,
+// and their bits i returned (on warp 0).
+template <bool kFp8>
+__device__ __noinline__ uint32_t clean_v(Smem& S, const Item& it, int blk, uint32_t chunk,
+                                         int st) {
+  constexpr int kDc = kFp8 ? 1 : 2;  // boxes across this CTA's 128 dimensions
+  auto row_piece = [&](int r, int piece) {  // 16-byte piece of key r of the block
+    const int kh = r / kChunkBoxRows;
+    const uint32_t slot = (chunk + (kFp8 ? 0 : kh)) % kSlots;
+    uint8_t* box = S.ring + slot * kSlotBytes + (kFp8 ? kh * kBoxBytes : (piece / 8) * kBoxBytes);
+    return reinterpret_cast<uint4*>(box + (r % kChunkBoxRows) * 128 + (piece % 8) * 16);
+  };
+  const int from = max(0, it.kend() - blk * kBlock);
+  const int n = (kBlock - from) * 8 * kDc;
+  for (int i = st; i < n; i += 32 * kSoftmaxWarps)
+    *row_piece(from + i / (8 * kDc), i % (8 * kDc)) = make_uint4(0, 0, 0, 0);
+  uint32_t bad = 0;
+  if (st < 32) {
+    for (int i = 0; i + 1 < it.ntok; ++i) {
+      const int r = it.p0 + 1 + i - blk * kBlock;
+      if (r < 0 || r >= kBlock) continue;
+      bool odd = false;
+      if (st < 8 * kDc) {
+        const uint4 v = *row_piece(r, st);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (kFp8) {
+            // a byte of 0x7F or 0xFF
+            const uint32_t y = (w[k] & 0x7F7F7F7Fu) + 0x01010101u;
+            odd |= (y & 0x80808080u) != 0;
+          } else {
+            odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+        bad |= 1u << i;
+        if (st < 8 * kDc) *row_piece(r, st) = make_uint4(0, 0, 0, 0);
+      }
+    }
   }
-  *reinterpret_cast<uint4*>(a.out + o_at) = make_uint4(w[0], w[1], w[2], w[3]);
+  return bad;
+}
+
+// The weights 2^(s - base) of the held-out keys p0 + 1 + i for this row, 0 where it does not
+// see them.
+template <bool kFp8>
+__device__ __noinline__ void late_weights(const ChunkAttnArgs& a, const Item& it, uint32_t bad,
+                                          int tok, int head, float base, float (&w)[3]) {
+  const float mul = a.scale * kLog2e * (kFp8 ? a.k_scale : 1.f);
+  for (int i = 0; i < 3; ++i) {
+    w[i] = 0.f;
+    const long long at = kv_row_index(a.kv[it.b], it.p0 + 1 + i);
+    if (!((bad >> i) & 1) || tok < i + 1 || tok >= it.ntok || at < 0) continue;
+    float s = 0.f;
+    for (int d = 0; d < kHeadDim; d += 8) {
+      float q[8], k[8];
+      load8<false>(a.q, (static_cast<long long>(it.row0 + tok) * kHeads + head) * kHeadDim + d, q);
+      load8<kFp8>(a.kv[it.b].k, at * kHeadDim + d, k);
+      for (int j = 0; j < 8; ++j) s = fmaf(q[j], k[j], s);
+    }
+    w[i] = ex2(fmaf(s, mul, -base));
+  }
+}
+
+template <bool kFp8>
+__device__ __noinline__ void add_late(const ChunkAttnArgs& a, const Item& it, const float (&w)[3],
+                                      uint32_t bad, int tok, int col, float (&o)[32]) {
+  for (int i = 0; i < 3; ++i) {
+    if (!((bad >> i) & 1) || tok < i + 1) continue;
+    const long long at = kv_row_index(a.kv[it.b], it.p0 + 1 + i);
+    if (at < 0) continue;
+#pragma unroll
+    for (int d = 0; d < 32; d += 8) {
+      float v[8];
+      load8<kFp8>(a.kv[it.b].v, at * kHeadDim + col + d, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[d + j] = fmaf(w[i], v[j], o[d + j]);
+    }
+  }
+}
+
+template <bool kFp8>
+__device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t rank,
+                            uint32_t tmem) {
+  using C = Cfg<kFp8>;
+  volatile int* abort = &S.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int swarp = warp - 2, st = threadIdx.x - 64;
+  const int quad = warp & 3, half = swarp >> 2;  // lanes of tensor memory; half of the keys
+  const int row = quad * 32 + lane;
+  const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t bar = 1 + quad;  // named barrier of the two warps that share these rows
+  const int tok = kCtaTokens * rank + row / kHeads;  // token of the tile
+  const int head = row % kHeads;
+  const float mul0 = a.scale * kLog2e * (kFp8 ? a.k_scale : 1.f);
+  const float v_mul = kFp8 ? a.v_scale : 1.f;
+  const uint32_t p_bar[2] = {map_to(&S.p_full[0], 0), map_to(&S.p_full[1], 0)};
+  const uint32_t o_bar = map_to(&S.o_free, 0);
+  const uint32_t q_bar = map_to(&S.q_full, 0);
+  uint32_t gt = 0, chunk = 0;
+  int item = 0;
+
+  // rows of refused sequences
+  for (int b = g; b < a.batch; b += gridDim.x / 2) {
+    if (S.plan.len[b] != -1) continue;
+    const size_t r0 = static_cast<size_t>(S.plan.start[b]) * (kQWidth / 8);
+    const size_t r1 = static_cast<size_t>(S.plan.start[b + 1]) * (kQWidth / 8);
+    uint4* out = reinterpret_cast<uint4*>(a.out);
+    for (size_t i = r0 + rank * 256 + st; i < r1; i += 512) out[i] = make_uint4(0, 0, 0, 0);
+  }
+  int2 info = make_int2(0, 0);  // for the combine kernel: rows of the tile and its parts
+
+  Cursor cur;
+  cur.init(S.plan, a.batch, g, G);
+  Item it;
+  while (cur.next(it)) {
+    const int n = it.blk1 - it.blk0;
+    float mul = mul0;
+    if constexpr (kFp8) {
+      const int e = split_q(S, a, it, rank, row, half, bar);
+      mul = mul0 * ldexpf(1.f, e);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) remote_arrive(q_bar);
+    }
+    // keys this row's token sees: positions below lim
+    const int lim = it.p0 + min(tok, it.ntok - 1) + 1;
+    float m = -INFINITY, base = 0.f, l = 0.f;  // m: raw; base = m mul (0 while m is -inf)
+    const float thr_step = C::kRescale / mul;
+    float thr = -INFINITY;
+    uint32_t bad_mine = 0;
+
+    for (int t = 0; t < n; ++t) {
+      const uint32_t j = (gt + t) & 1;
+      const int blk = it.blk0 + t;
+      const bool special = blk >= it.special();
+      const uint32_t sa = tmem + lane_addr + kTmemS + kBlock * j;
+      mbar_wait(&S.s_full[j], ((gt + t) >> 1) & 1, abort);
+      tc_fence_after();
+      float s[64];
+      {
+        uint32_t r0[32], r1[32];
+        tmem_ld_32x32b_x32(sa + 64 * half, r0);
+        tmem_ld_32x32b_x32(sa + 64 * half + 32, r1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r0[i]), s[32 + i] = __uint_as_float(r1[i]);
+      }
+      const int left = lim - (blk * kBlock + 64 * half);  // of these 64 keys, those below it
+      if (special) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : -INFINITY;
+      }
+      float mx = s[0];
+      {
+        float m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+        for (int i = 4; i < 64; i += 4) {
+          mx = fmaxf(mx, s[i]);
+          m1 = fmaxf(m1, s[i + 1]);
+          m2 = fmaxf(m2, s[i + 2]);
+          m3 = fmaxf(m3, s[i + 3]);
+        }
+        mx = fmaxf(fmaxf(mx, m1), fmaxf(m2, m3));
+      }
+      // (also: both warps have read their scores, which P will overwrite)
+      if (named_bar_or(bar, 64, mx > thr)) {
+        S.xch[half][row] = mx;
+        named_bar_sync(bar, 64);
+        const float mn = fmaxf(m, fmaxf(mx, S.xch[half ^ 1][row]));
+        const float alpha = m == mn ? 1.f : ex2((m - mn) * mul);
+        m = mn;
+        base = mn == -INFINITY ? 0.f : mn * mul;
+        thr = mn + thr_step;
+        l *= alpha;
+        if (t > 0) {
+          // O holds PV(t - 1) before it is rescaled
+          mbar_wait(&S.pv_done[(gt + t - 1) & 1], ((gt + t - 1) >> 1) & 1, abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            const uint32_t oa = tmem + lane_addr + kTmemO + 128 * half + 32 * c;
+            tmem_ld_32x32b_x32(oa, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st_32x32b_x32(oa, o);
+          }
+        }
+      }
+      const float off = base - C::kPExp;
+      uint32_t pw[32];
+      float l1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        // a hidden key's score is -inf: its weight is 0
+        const float p0 = ex2(fmaf(s[2 * i], mul, -off)), p1 = ex2(fmaf(s[2 * i + 1], mul, -off));
+        l += p0;
+        l1 += p1;
+        pw[i] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+      }
+      l += l1;
+      if constexpr (kFp8) {
+        uint32_t hl[32];  // 16 words of high parts, 16 of low parts
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          uint32_t h0, l0, h1, l1w;
+          split_e4m3x2(pw[2 * i], h0, l0);
+          split_e4m3x2(pw[2 * i + 1], h1, l1w);
+          hl[i] = h0 | (h1 << 16);
+          hl[16 + i] = l0 | (l1w << 16);
+        }
+        uint32_t w0[16], w1[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w0[i] = hl[i], w1[i] = hl[16 + i];
+        tmem_st_32x32b_x16(sa + 16 * half, w0);
+        tmem_st_32x32b_x16(sa + 32 + 16 * half, w1);
+      } else {
+        tmem_st_32x32b_x32(sa + 32 * half, pw);
+      }
+      tmem_wait_st();
+      if (special) {
+        // the V half of this block, before the product may read it
+        const uint32_t vc = chunk + C::kKSlots + t * (C::kKSlots + C::kVSlots) +
+                            (t + 1 < n ? C::kKSlots : 0);
+#pragma unroll
+        for (int c = 0; c < C::kVSlots; ++c)
+          mbar_wait(&S.v_full[(vc + c) % kSlots], ((vc + c) / kSlots) & 1, abort);
+        if (!*abort) {
+          bad_mine |= clean_v<kFp8>(S, it, blk, vc, st);
+          if (swarp == 0 && lane < 2) remote_store(map_to(&S.bad[item & 1][rank], lane), bad_mine);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) remote_arrive(p_bar[j]);
+    }
+    gt += n;
+    chunk += n * (C::kKSlots + C::kVSlots);
+
+    // ---- epilogue ----
+    S.xch[half][row] = l;
+    named_bar_sync(bar, 64);
+    l += S.xch[half ^ 1][row];
+    mbar_wait(&S.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort);
+    tc_fence_after();
+    const bool ok = *abort == 0;
+    const uint32_t bad = it.blk1 > it.special() ? S.bad[item & 1][half] : 0u;
+    float late[3] = {0.f, 0.f, 0.f};
+    if (bad != 0) late_weights<kFp8>(a, it, bad, tok, head, base - C::kPExp, late);
+    const bool real = tok < it.ntok;
+    const bool whole = it.whole();
+    const int slot = 2 * g + (it.blk0 == 0 ? 1 : 0);
+    const float inv = v_mul / l;
+    uint16_t* out = a.out + (static_cast<size_t>(it.row0 + tok) * kHeads + head) * kHeadDim + 128 * half;
+    float* acc = slot_acc(a.partials, slot) + (rank * kRows + row) * kHeadDim + 128 * half;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem + lane_addr + kTmemO + 128 * half + 32 * c, r);
+      tmem_wait_ld();
+      if (c == 3) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive(o_bar);
+      }
+      float o[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
+      if (bad != 0) add_late<kFp8>(a, it, late, bad, tok, 128 * half + 32 * c, o);
+      if (!ok || !real) continue;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
+              make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                         pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(acc + 32 * c + 4 * i) =
+              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+    }
+    if (!whole) {
+      if (ok && real && half == 0) {
+        // (a part none of whose keys the row sees: m stays -inf, its weight will be 0)
+        slot_m(a.partials, slot)[rank * kRows + row] = m == -INFINITY ? -INFINITY : base;
+        slot_l(a.partials, slot)[rank * kRows + row] = l;
+      }
+      if (it.blk0 == 0) {
+        const int total = S.plan.cost[a.batch];
+        const int last = range_of(it.cost0 + kTileCost + it.nblk - 1, G, total);
+        info = make_int2(it.row0, (last - g + 1) * 8 + it.ntok);
+      }
+    }
+    // (the next item writes xch only behind this pair's next barrier)
+    named_bar_sync(bar, 64);
+    ++item;
+  }
+  if (rank == 0 && st == 0) a.info[g] = info;
+}
+
+template <bool kFp8, bool kPaged>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ ChunkAttnArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                     ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = cta_rank();
+  const int g = blockIdx.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&S.kv_full[i], 1);
+      mbar_init(&S.kv_empty[i], 1);
+      mbar_init(&S.v_full[i], 1);
+    }
+    mbar_init(&S.q_full, kFp8 ? 2 * kSoftmaxWarps : 1);
+    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.p_full[i], 2 * kSoftmaxWarps);
+    }
+    mbar_init(&S.o_free, 2 * kSoftmaxWarps);
+    mbar_init(&S.mma_done, 1);
+    S.abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&q_map);
+  }
+  if (warp == 1) pair_tmem_alloc(&S.tmem_base);
+  pdl_launch_dependents();
+  pdl_wait();
+  build_plan(S, a, blockIdx.x == 0);
+  const int G = min(static_cast<int>(gridDim.x) / 2, S.plan.cost[a.batch]);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers are set up (and a CTA-wide barrier)
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == 0) {
+    run_producer<kFp8, kPaged>(S, &q_map, a, g, G, rank);
+  } else if (warp == 1) {
+    if (rank == 0) run_mma<kFp8>(S, a, g, G, tmem);
+  } else {
+    run_softmax<kFp8>(S, a, g, G, rank, tmem);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && S.abort_flag) atomicOr(a.err, kErrTimeout);
+  __syncwarp();
+  cluster_sync();  // the other CTA's products and arrivals are done with this one's memory
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    pair_tmem_dealloc(tmem);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// merge of the tiles that several pairs share: one warp a row, fixed order
+// ---------------------------------------------------------------------------------------
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(ChunkAttnArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int g = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);  // of the tile's 256
+  const int2 info = __ldcg(&a.info[g]);
+  const int parts = info.y >> 3, ntok = info.y & 7;
+  if (row >= ntok * kHeads) return;
+  // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
+  auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(slot_m(a.partials, slot(i)) + row));
+  M = warp_max_f32(M);
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, o[8] = {};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float* acc = slot_acc(a.partials, slot(i)) + row * kHeadDim + 8 * lane;
+    const float w = ex2(__ldcg(slot_m(a.partials, slot(i)) + row) - base);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(acc));
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(acc + 4));
+    L = fmaf(w, __ldcg(slot_l(a.partials, slot(i)) + row), L);
+    o[0] = fmaf(w, x.x, o[0]), o[1] = fmaf(w, x.y, o[1]);
+    o[2] = fmaf(w, x.z, o[2]), o[3] = fmaf(w, x.w, o[3]);
+    o[4] = fmaf(w, y.x, o[4]), o[5] = fmaf(w, y.y, o[5]);
+    o[6] = fmaf(w, y.z, o[6]), o[7] = fmaf(w, y.w, o[7]);
+  }
+  const float inv = (a.kv_dtype == MFA_KV_FP8_E4M3 ? a.v_scale : 1.f) / L;
+  uint16_t* out = a.out + (static_cast<size_t>(info.x) * kHeads + row) * kHeadDim + 8 * lane;
+  *reinterpret_cast<uint4*>(out) =
+      make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                 pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+}
+
+using Kernel = void (*)(CUtensorMap, ChunkAttnArgs);
+constexpr int kSmemBytes = sizeof(Smem) + 1024;
+
+// The kernel of a call's cache type and layout, its shared-memory limit raised; null on error.
+Kernel kernel_of(const ChunkAttnArgs& a) {
+  const Kernel all[4] = {chunk_attn_kernel<false, false>, chunk_attn_kernel<false, true>,
+                         chunk_attn_kernel<true, false>, chunk_attn_kernel<true, true>};
+  static std::atomic<uint64_t> smem_set[4];
+  const int i = 2 * (a.kv_dtype == MFA_KV_FP8_E4M3) + (a.page_size != 0);
+  if (!set_smem_limit_once(reinterpret_cast<const void*>(all[i]), kSmemBytes, &smem_set[i]))
+    return nullptr;
+  return all[i];
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t s) {
-  return launch_pdl(chunk_attn_kernel, dim3(a.n_rows, kHeads / 8), dim3(256), 0, s, a);
+int chunk_attn_pairs(const ChunkAttnArgs& a) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  static std::atomic<int> cached[64];
+  const bool known = dev >= 0 && dev < 64;
+  if (known && cached[dev].load() > 0) return cached[dev].load();
+  const Kernel kernel = kernel_of(a);
+  if (kernel == nullptr) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kMaxAttnGrid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  int n = 0;
+  // (every instantiation fills an SM alike: one CTA of kSmemBytes)
+  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kernel), &cfg) != cudaSuccess)
+    return 0;
+  if (known) cached[dev].store(n);
+  return n;
+}
+
+cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const ChunkAttnArgs& a, cudaStream_t s) {
+  const Kernel kernel = kernel_of(a);
+  if (kernel == nullptr) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      launch_pdl(kernel, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, q_map, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_combine_kernel, dim3(a.pairs, kChunkRows / kCombineWarps),
+                    dim3(32 * kCombineWarps), 0, s, a);
 }
 
 }  // namespace mfa

@@ -145,14 +145,16 @@ inline WsLayout ws_layout(int batch, int num_sms) {
 }
 
 // The chunk attention's partials follow the workspace of the other calls: its work is cut
-// into contiguous ranges over pairs of SMs, and a range has at most two items that end inside
-// a tile, its first and its last (chunk_attn.cu), so two slots of 256 rows -- 4 tokens x 64
-// heads, running maximum and sum and the 256 accumulators of each, fp32 -- per pair.
+// into contiguous ranges over pairs of SMs, and a range has at most two items that do not
+// cover their tile, its first and its last (chunk_attn.cu), so two slots of 256 rows -- 4
+// tokens x 64 heads, running maximum and sum and the 256 accumulators of each, fp32 -- per
+// pair, and the merge's 8 bytes a pair.
 constexpr int kChunkRows = 256;
 constexpr size_t kChunkPartialFloats = (size_t)kChunkRows * (2 + kHeadDim);
 inline int chunk_grid_for(int num_sms) { return num_sms / 2; }
 inline size_t chunk_ws_bytes(const WsLayout& L, int num_sms) {
-  return L.total + 2 * (size_t)chunk_grid_for(num_sms) * kChunkPartialFloats * sizeof(float);
+  return L.total + (size_t)chunk_grid_for(num_sms) *
+                       (2 * kChunkPartialFloats * sizeof(float) + sizeof(int2));
 }
 
 // Launch with programmatic stream serialization: the kernel may start while the previous
@@ -303,10 +305,16 @@ struct ChunkAttnArgs {
   int batch, n_rows;
   float scale;
   uint16_t* out;            // [n_rows, 64, 256] bf16
-  float* partials;
+  float* partials;          // two slots of kChunkPartialFloats per pair
+  int2* info;               // [pairs]: the split tile that begins in a pair, for the merge
   uint32_t* err;
+  int pairs;                // CTA pairs of the grid
 };
-cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t s);
+// q_map covers q as [n_rows * 64 rows, 256] bf16, boxes of [128 rows x 64 dims], 128-byte
+// swizzle.
+cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const ChunkAttnArgs& a, cudaStream_t s);
+// CTA pairs that can be resident on the current device at once (0 on an error).
+int chunk_attn_pairs(const ChunkAttnArgs& a);
 
 // One CTA whose bounded wait on a barrier that nothing completes gives up after limit_us
 // and sets kErrTimeout in *err (selftest.cu).

@@ -333,8 +333,8 @@ MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, c
  * mfa_decode_attn; long and short chunks may share a call. Cache rows that a token does not
  * see (later tokens, rows past the sequence's end) may hold any bytes, infinities and NaN
  * included, and do not reach its result. For FP8 caches the cached codes are used exactly, q
- * and the softmax weights as in mfa_decode_attn (q with one power-of-two scale per token and
- * head).
+ * as in mfa_decode_attn with one power-of-two scale per token and head, and the softmax weights
+ * as e4m3 pairs within 2^-8 of their value or 2^-14 of the row's largest weight.
  * q: device bf16 [n_rows, 64, 256]; out: device bf16 [n_rows, 64, 256]; scale > 0.
  * kv: a table of mfa_chunk_table_bytes(kv->batch) bytes or more.
  * ws: device workspace of mfa_chunk_workspace_bytes(kv->batch) bytes (initialized once).

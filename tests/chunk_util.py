@@ -37,7 +37,7 @@ def angles(table, rot_dim, pair_axis, positions):
 
 def attention(q, k, v, first, scale):
     """q [n, 64, 256] float64 of positions first .. first + n - 1, k and v [L, 256] float64:
-    (out, weight of |V|: the same with absolute values, for the tolerance)."""
+    (out; for the tolerance: the same of |V|, and the largest weight times the sum of |V|)."""
     n, length = q.shape[0], k.shape[0]
     s = torch.einsum("nhd,ld->nhl", q, k) * scale
     seen = torch.arange(length, device=q.device)[None] <= \
@@ -46,12 +46,13 @@ def attention(q, k, v, first, scale):
     p = torch.softmax(s, -1)
     # (a hidden row's values do not take part, whatever they are)
     out = torch.empty(n, HEADS, DIM, dtype=F64, device=q.device)
-    mag = torch.empty_like(out)
+    mag, top = torch.empty_like(out), torch.empty_like(out)
     for i in range(n):
         end = first + i + 1
         out[i] = p[i, :, :end] @ v[:end]
         mag[i] = p[i, :, :end] @ v[:end].abs()
-    return out, mag
+        top[i] = p[i].amax(-1, keepdim=True) * v[:end].abs().sum(0)
+    return out, mag, top
 
 
 # ---------------------------------------------------------------------- ragged batches
@@ -151,7 +152,7 @@ class Batch:
             rows = slice(self.starts[b], self.starts[b + 1])
             q = self.q[rows].to(F64)
             k, v = self.values("k", b), self.values("v", b)
-            o, mag = attention(q, k, v, self.cached[b], scale)
+            o, mag, top = attention(q, k, v, self.cached[b], scale)
             out[rows] = o
             # one rounding of the result (half a bf16 step: 2^-8 of it); the weights rounded
             # to bf16, or to an e4m3 pair within 2^-8 of them; a score's 256 products are
@@ -162,8 +163,13 @@ class Batch:
             if self.fp8:
                 # q as an e4m3 pair: exact within 2^-10 of the row's largest, half the
                 # smallest step of the low part (2^-10 of a largest of at least 128) below
-                top = q.abs().amax(-1, keepdim=True)
-                score = score + 2.0 ** -17 * top * k.abs().sum(-1).max() * scale
+                qmax = q.abs().amax(-1, keepdim=True)
+                score = score + 2.0 ** -17 * qmax * k.abs().sum(-1).max() * scale
+                # a weight p is the e4m3 pair of 2^(s - m + 4), m at most the row's largest
+                # score: the largest is 2^4 or more. A pair is off by at most half a step of
+                # its low part: 2^-8 of p, or, where that is subnormal, half of 2^-9, which is
+                # at most 2^-14 of the largest weight
+                mag = mag + 2.0 ** -6 * top
             tol[rows] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2 * score) * mag + 1e-30
         return out, tol
 

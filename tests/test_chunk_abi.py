@@ -83,16 +83,16 @@ def test_binding_refusals():
     q = torch.zeros(4, 64, 256, dtype=torch.bfloat16)
     kv = torch.zeros(4, 512, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="q_start"):
-        mfa.chunk_attn(q, cache, starts[:2], lens, ws=1)
+        mfa.chunk_attn(q, cache, starts[:2], lens, ws=mfa)
     with pytest.raises(ValueError, match="seq_lens"):
-        mfa.chunk_attn(q, cache, starts, lens.long(), ws=1)
+        mfa.chunk_attn(q, cache, starts, lens.long(), ws=mfa)
     for bad in (q.float(), q[:, :32], q.view(4, 256, 64)):
         with pytest.raises(ValueError, match="q must be"):
             mfa.chunk_attn(bad, cache, starts, lens, out=q, ws=mfa)
     with pytest.raises(ValueError, match="CUDA"):
         mfa.chunk_attn(q, cache, starts, lens, out=q, ws=mfa)
     with pytest.raises(ValueError, match="k must be"):
-        mfa.rope_append(q, kv[:, :256], kv[:, 256:], cache, starts, lens, ws=1)
+        mfa.rope_append(q, kv[:, :256], kv[:, 256:], cache, starts, lens, ws=mfa)
     with pytest.raises(ValueError, match="rot_dim"):
         mfa.Rope(torch.zeros(5, 24))
     with pytest.raises(ValueError, match="float32"):
@@ -118,7 +118,7 @@ def test_plain_attention_is_the_oracle_s():
     g = torch.Generator().manual_seed(1)
     q = torch.randn(3, 64, 256, generator=g, dtype=torch.float64)
     k, v = (torch.randn(9, 256, generator=g, dtype=torch.float64) for _ in range(2))
-    out, mag = cu.attention(q, k, v, 6, 1 / 16)
+    out, mag, _ = cu.attention(q, k, v, 6, 1 / 16)
     for i in range(3):
         want = omfa.decode_attn_seq(q[i].numpy(), k[:7 + i].numpy(), v[:7 + i].numpy(), 1 / 16)
         assert abs(out[i].numpy() - want).max() < 1e-12
