@@ -74,6 +74,7 @@ struct Cfg {
   static constexpr int kVSlots = kFp8 ? 1 : 2;
   static constexpr float kRescale = kFp8 ? 4.0f : 8.0f;  // log2 units
   static constexpr float kPExp = kFp8 ? 4.0f : 0.0f;     // P = 2^(s - m + kPExp)
+  static constexpr int kPolyEvery = 4;  // pairs of weights per pair by polynomial
   static constexpr uint32_t kIdescS = idesc_f16(256, kBlock, !kFp8, false, false);
   static constexpr uint32_t kIdescPV = idesc_f16(256, kHeadDim, !kFp8, false, true);
 };
@@ -118,6 +119,21 @@ __device__ __forceinline__ void cluster_sync() {
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// True on one lane of the (converged) warp. Unlike a lane test, it tells the compiler that one
+// thread runs what depends on it: descriptors then go through uniform registers, and eight
+// products are issued in ~100 cycles instead of ~500 (they take the tensor core 512).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // shared::cluster address of this CTA's `p` in CTA `rank` of the pair
 __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
   uint32_t r;
@@ -125,44 +141,19 @@ __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
   return r;
 }
 
+// Arrive on a barrier of either CTA. The plain form orders what tensor memory needs (with
+// tcgen05.fence) and nothing that the other CTA reads from shared memory; the release form also
+// does that, and waits for a fence of ~1000 cycles, so it is for special blocks only.
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void remote_arrive_release(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
 
 __device__ __forceinline__ void remote_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// As mbar_wait, for arrivals that come from the other CTA too.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
-                                             volatile int* abort) {
-  if (*abort) return false;
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort) return false;
-      if (globaltimer() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
 }
 
 __device__ __forceinline__ uint64_t policy_evict_normal() {
@@ -214,42 +205,60 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       : "memory");
 }
 
+// Shared-memory matrix descriptors of the tiles here (128-byte swizzle, 8-row groups 1024 bytes
+// apart): the low word, to which a byte offset of x adds x / 16, and the constant high word.
+// lbo: the distance of 64-element column groups of an MN-major operand (else ignored).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
 // D[tmem] (+)= A . B over the pair; A in shared memory (SS) or tensor memory (TS).
 template <bool kFp8>
-__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                             uint32_t acc) {
   if constexpr (kFp8)
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
+        ".reg .b64 a, b;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+        "mov.b64 a, {%1, %5};\n"
+        "mov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi) : "memory");
   else
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
+        ".reg .b64 a, b;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+        "mov.b64 a, {%1, %5};\n"
+        "mov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi) : "memory");
 }
 template <bool kFp8>
-__device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc,
+__device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
                                             uint32_t acc) {
   if constexpr (kFp8)
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
+        ".reg .b64 b;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d), "r"(a), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+        "mov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], b, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi) : "memory");
   else
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
+        ".reg .b64 b;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d), "r"(a), "l"(bd), "r"(idesc), "r"(acc) : "memory");
+        "mov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi) : "memory");
 }
 
 // ---------------------------------------------------------------------------------------
@@ -459,7 +468,7 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
   const int lane = threadIdx.x & 31;
-  const bool leader = lane == 0;
+  const bool leader = elect_one();
   const KvChunkMaps* maps = reinterpret_cast<const KvChunkMaps*>(a.kv + a.batch);
   const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
   const uint32_t q_bar = map_to(&S.q_full, 0);
@@ -580,37 +589,35 @@ template <bool kFp8>
 __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t tmem) {
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
-  const bool leader = (threadIdx.x & 31) == 0;
+  const bool leader = elect_one();
   uint32_t chunk = 0, gt = 0;
   int item = 0;
-  const uint32_t q_base = smem_u32(S.q), ring = smem_u32(S.ring);
+  const uint32_t q_lo = desc_lo(smem_u32(S.q), 16), ring = smem_u32(S.ring);
 
   auto issue_s = [&](uint32_t t) {
     const uint32_t d = tmem + kTmemS + kBlock * (t & 1);
 #pragma unroll
     for (int c = 0; c < C::kKSlots; ++c, ++chunk) {
       const uint32_t slot = chunk % kSlots;
-      wait_cluster(&S.kv_full[slot], (chunk / kSlots) & 1, abort);
+      mbar_wait(&S.kv_full[slot], (chunk / kSlots) & 1, abort);
       tc_fence_after();
       if (leader && !*abort) {
-        const uint32_t kb = ring + slot * kSlotBytes;
+        const uint32_t k_lo = desc_lo(ring + slot * kSlotBytes, 16);
         if constexpr (kFp8) {
           // high parts, then low parts of Q, over the same keys
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int part = i >> 3, box = (i >> 2) & 1, kk = i & 3;
-            pair_mma_ss<true>(
-                d, sdesc_sw128(q_base + (2 * part + box) * kQChunkBytes + 32 * kk, 16, 1024),
-                sdesc_sw128(kb + box * kBoxBytes + 32 * kk, 16, 1024), C::kIdescS, i != 0);
+            pair_mma_ss<true>(d, q_lo + ((2 * part + box) * kQChunkBytes + 32 * kk) / 16,
+                              k_lo + (box * kBoxBytes + 32 * kk) / 16, C::kIdescS, i != 0);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int box = i >> 2, kk = i & 3;
-            pair_mma_ss<false>(
-                d, sdesc_sw128(q_base + (2 * c + box) * kQChunkBytes + 32 * kk, 16, 1024),
-                sdesc_sw128(kb + box * kBoxBytes + 32 * kk, 16, 1024), C::kIdescS,
-                (c | i) != 0);
+            pair_mma_ss<false>(d, q_lo + ((2 * c + box) * kQChunkBytes + 32 * kk) / 16,
+                               k_lo + (box * kBoxBytes + 32 * kk) / 16, C::kIdescS,
+                               (c | i) != 0);
           }
         }
         pair_commit(&S.kv_empty[slot]);
@@ -620,34 +627,38 @@ __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t 
   };
 
   auto issue_pv = [&](uint32_t t, bool first) {
-    wait_cluster(&S.p_full[t & 1], (t >> 1) & 1, abort);
-    if (first && item > 0) wait_cluster(&S.o_free, (item - 1) & 1, abort);
-    tc_fence_after();
-    const uint32_t d = tmem + kTmemO, p = tmem + kTmemS + kBlock * (t & 1);
+    // V first: it has landed long before P, and a wait costs ~150 cycles even so
+    uint32_t v_lo[C::kVSlots], slot[C::kVSlots];
 #pragma unroll
     for (int c = 0; c < C::kVSlots; ++c, ++chunk) {
-      const uint32_t slot = chunk % kSlots;
-      wait_cluster(&S.kv_full[slot], (chunk / kSlots) & 1, abort);
-      tc_fence_after();
-      if (leader && !*abort) {
-        const uint32_t vb = ring + slot * kSlotBytes;
+      slot[c] = chunk % kSlots;
+      mbar_wait(&S.kv_full[slot[c]], (chunk / kSlots) & 1, abort);
+      v_lo[c] = desc_lo(ring + slot[c] * kSlotBytes, kBoxBytes);
+    }
+    if (first && item > 0) mbar_wait(&S.o_free, (item - 1) & 1, abort);
+    mbar_wait(&S.p_full[t & 1], (t >> 1) & 1, abort);
+    tc_fence_after();
+    const uint32_t d = tmem + kTmemO, p = tmem + kTmemS + kBlock * (t & 1);
+    if (leader && !*abort) {
+#pragma unroll
+      for (int c = 0; c < C::kVSlots; ++c) {
         if constexpr (kFp8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int part = i >> 2, kt = i & 3;  // 32 keys each
-            pair_mma_ts<true>(d, p + 32 * part + 8 * kt, sdesc_sw128(vb + 4096 * kt, kBoxBytes, 1024),
-                              C::kIdescPV, !(first && i == 0));
+            pair_mma_ts<true>(d, p + 32 * part + 8 * kt, v_lo[c] + 4096 * kt / 16, C::kIdescPV,
+                              !(first && i == 0));
           }
         } else {
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt)  // 16 keys each
-            pair_mma_ts<false>(d, p + 8 * (4 * c + kt), sdesc_sw128(vb + 2048 * kt, kBoxBytes, 1024),
-                               C::kIdescPV, !(first && c == 0 && kt == 0));
+            pair_mma_ts<false>(d, p + 8 * (4 * c + kt), v_lo[c] + 2048 * kt / 16, C::kIdescPV,
+                               !(first && c == 0 && kt == 0));
         }
-        pair_commit(&S.kv_empty[slot]);
+        pair_commit(&S.kv_empty[slot[c]]);
       }
+      pair_commit(&S.pv_done[t & 1]);
     }
-    if (leader && !*abort) pair_commit(&S.pv_done[t & 1]);
   };
 
   Cursor cur;
@@ -655,7 +666,7 @@ __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t 
   Item it;
   while (cur.next(it)) {
     const int n = it.blk1 - it.blk0;
-    wait_cluster(&S.q_full, item & 1, abort);
+    mbar_wait(&S.q_full, item & 1, abort);
     tc_fence_after();
     issue_s(gt);
     for (int t = 0; t < n; ++t) {
@@ -690,6 +701,56 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The larger of three, NaN if one is: a row with a NaN score gets a NaN maximum, so every
+// weight of it is NaN (the polynomial below would lose it).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two floats at a time.
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair_f32(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of two values without the special-function unit, which the softmax keeps busy for as long
+// as one of the two products of a block takes (64 weights a thread, 16 a cycle and SM): x = n + f
+// with n the nearest whole number (added to and taken from 1.5 x 2^23), 2^f for |f| <= 1/2 by a
+// cubic with p(0) = 1 fitted for the least largest relative error (1.0e-4, a twentieth of the
+// bf16 rounding that follows), n added to the exponent. x <= 8; below -127 it gives 0.
+__device__ __forceinline__ void exp2_poly2(uint64_t x, float& y0, float& y1) {
+  float x0, x1;
+  unpair_f32(x, x0, x1);
+  x = pair_f32(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+  const uint64_t t = add2(x, pair_f32(12582912.f, 12582912.f));
+  const uint64_t n = add2(t, pair_f32(-12582912.f, -12582912.f));
+  const uint64_t f = fma2(n, pair_f32(-1.f, -1.f), x);
+  uint64_t p = fma2(pair_f32(0.05500893f, 0.05500893f), f, pair_f32(0.24221096f, 0.24221096f));
+  p = fma2(p, f, pair_f32(0.69328293f, 0.69328293f));
+  p = fma2(p, f, pair_f32(1.f, 1.f));
+  float t0, t1, p0, p1;
+  unpair_f32(t, t0, t1);
+  unpair_f32(p, p0, p1);
+  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
 // f16x2 as e4m3 high and low parts: hi = e4m3(v), lo = e4m3(v - hi) (exact difference)
 __device__ __forceinline__ void split_e4m3x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
   uint16_t h, l;
@@ -847,19 +908,53 @@ __device__ __noinline__ void late_weights(const ChunkAttnArgs& a, const Item& it
   }
 }
 
+// Rows that were held out of the products, added to this thread's half of its row of O in
+// tensor memory.
 template <bool kFp8>
-__device__ __noinline__ void add_late(const ChunkAttnArgs& a, const Item& it, const float (&w)[3],
-                                      uint32_t bad, int tok, int col, float (&o)[32]) {
-  for (int i = 0; i < 3; ++i) {
-    if (!((bad >> i) & 1) || tok < i + 1) continue;
-    const long long at = kv_row_index(a.kv[it.b], it.p0 + 1 + i);
-    if (at < 0) continue;
+__device__ __noinline__ void add_late(const ChunkAttnArgs& a, const Item& it, uint32_t bad, int tok,
+                                      int head, int half, float base, uint32_t o_addr) {
+  float w[3];
+  late_weights<kFp8>(a, it, bad, tok, head, base, w);
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    uint32_t o[16];
+    tmem_ld_32x32b_x16(o_addr + 16 * c, o);
+    tmem_wait_ld();
+    for (int i = 0; i < 3; ++i) {
+      if (!((bad >> i) & 1) || tok < i + 1 || tok >= it.ntok) continue;
+      const long long at = kv_row_index(a.kv[it.b], it.p0 + 1 + i);
+      if (at < 0) continue;
 #pragma unroll
-    for (int d = 0; d < 32; d += 8) {
-      float v[8];
-      load8<kFp8>(a.kv[it.b].v, at * kHeadDim + col + d, v);
+      for (int d = 0; d < 16; d += 8) {
+        float v[8];
+        load8<kFp8>(a.kv[it.b].v, at * kHeadDim + 128 * half + 16 * c + d, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[d + j] = fmaf(w[i], v[j], o[d + j]);
+        for (int j = 0; j < 8; ++j)
+          o[d + j] = __float_as_uint(fmaf(w[i], v[j], __uint_as_float(o[d + j])));
+      }
+    }
+    __syncwarp();
+    tmem_st_32x32b_x16(o_addr + 16 * c, o);
+  }
+  tmem_wait_st();
+}
+
+// 16-byte pieces: lane i of a group of eight has piece j of its own row in w[4 j ..]; after it,
+// piece i of row j of the group there.
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[32], int lane) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j & d) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t& x = w[4 * j + k];
+        uint32_t& y = w[4 * (j | d) + k];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x : y, d);
+        (up ? x : y) = got;
+      }
     }
   }
 }
@@ -906,7 +1001,7 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
       mul = mul0 * ldexpf(1.f, e);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) remote_arrive(q_bar);
+      if (lane == 0) remote_arrive_release(q_bar);
     }
     // keys this row's token sees: positions below lim
     const int lim = it.p0 + min(tok, it.ntok - 1) + 1;
@@ -936,26 +1031,26 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
 #pragma unroll
         for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : -INFINITY;
       }
-      float mx = s[0];
+      float mx = max3(s[0], s[1], s[2]);
       {
-        float m1 = s[1], m2 = s[2], m3 = s[3];
+        float m1 = max3(s[3], s[4], s[5]);
 #pragma unroll
-        for (int i = 4; i < 64; i += 4) {
-          mx = fmaxf(mx, s[i]);
-          m1 = fmaxf(m1, s[i + 1]);
-          m2 = fmaxf(m2, s[i + 2]);
-          m3 = fmaxf(m3, s[i + 3]);
+        for (int i = 6; i < 62; i += 4) {
+          mx = max3(mx, s[i], s[i + 1]);
+          m1 = max3(m1, s[i + 2], s[i + 3]);
         }
-        mx = fmaxf(fmaxf(mx, m1), fmaxf(m2, m3));
+        mx = max3(max3(mx, m1, s[62]), s[63], s[63]);
       }
       // (also: both warps have read their scores, which P will overwrite)
-      if (named_bar_or(bar, 64, mx > thr)) {
+      // (a NaN maximum counts as a larger one, once)
+      if (named_bar_or(bar, 64, !(mx <= thr) && m == m)) {
         S.xch[half][row] = mx;
         named_bar_sync(bar, 64);
-        const float mn = fmaxf(m, fmaxf(mx, S.xch[half ^ 1][row]));
+        const float mn = max3(m, mx, S.xch[half ^ 1][row]);
         const float alpha = m == mn ? 1.f : ex2((m - mn) * mul);
         m = mn;
-        base = mn == -INFINITY ? 0.f : mn * mul;
+        // an infinite maximum makes the row's weights NaN (inf - inf), as the softmax's are
+        base = mn == -INFINITY ? 0.f : mn * mul + (mn - mn);
         thr = mn + thr_step;
         l *= alpha;
         if (t > 0) {
@@ -974,18 +1069,30 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
           }
         }
       }
-      const float off = base - C::kPExp;
+      // weights 2^(s - base), one of kPolyEvery pairs by polynomial; a hidden key's score is
+      // -inf and its weight 0
+      const uint64_t mul2 = pair_f32(mul, mul), off2 = pair_f32(C::kPExp - base, C::kPExp - base);
       uint32_t pw[32];
-      float l1 = 0.f;
+      uint64_t l2 = pair_f32(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        // a hidden key's score is -inf: its weight is 0
-        const float p0 = ex2(fmaf(s[2 * i], mul, -off)), p1 = ex2(fmaf(s[2 * i + 1], mul, -off));
-        l += p0;
-        l1 += p1;
+        const uint64_t x = fma2(pair_f32(s[2 * i], s[2 * i + 1]), mul2, off2);
+        float p0, p1;
+        if (i % C::kPolyEvery == C::kPolyEvery - 1) {
+          exp2_poly2(x, p0, p1);
+        } else {
+          unpair_f32(x, p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+        }
+        l2 = add2(l2, pair_f32(p0, p1));
         pw[i] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
       }
-      l += l1;
+      {
+        float l0, l1;
+        unpair_f32(l2, l0, l1);
+        l += l0 + l1;
+      }
       if constexpr (kFp8) {
         uint32_t hl[32];  // 16 words of high parts, 16 of low parts
 #pragma unroll
@@ -1012,15 +1119,19 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
 #pragma unroll
         for (int c = 0; c < C::kVSlots; ++c)
           mbar_wait(&S.v_full[(vc + c) % kSlots], ((vc + c) / kSlots) & 1, abort);
-        if (!*abort) {
-          bad_mine |= clean_v<kFp8>(S, it, blk, vc, st);
-          if (swarp == 0 && lane < 2) remote_store(map_to(&S.bad[item & 1][rank], lane), bad_mine);
-        }
+        if (!*abort) bad_mine |= clean_v<kFp8>(S, it, blk, vc, st);
+        if (bad_mine != 0 && lane < 2)  // (warp 0) for the epilogues of both CTAs
+          remote_store(map_to(&S.bad[item & 1][rank], lane), bad_mine);
         fence_proxy_async_smem();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) remote_arrive(p_bar[j]);
+      if (lane == 0) {
+        if (bad_mine != 0)
+          remote_arrive_release(p_bar[j]);
+        else
+          remote_arrive(p_bar[j]);
+      }
     }
     gt += n;
     chunk += n * (C::kKSlots + C::kVSlots);
@@ -1032,43 +1143,63 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     mbar_wait(&S.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort);
     tc_fence_after();
     const bool ok = *abort == 0;
-    const uint32_t bad = it.blk1 > it.special() ? S.bad[item & 1][half] : 0u;
-    float late[3] = {0.f, 0.f, 0.f};
-    if (bad != 0) late_weights<kFp8>(a, it, bad, tok, head, base - C::kPExp, late);
-    const bool real = tok < it.ntok;
+    const uint32_t o_addr = tmem + lane_addr + kTmemO + 128 * half;
+    // (volatile: written by the other CTA too)
+    const uint32_t bad = *static_cast<volatile uint32_t*>(&S.bad[item & 1][half]);
+    if (bad != 0) add_late<kFp8>(a, it, bad, tok, head, half, base - C::kPExp, o_addr);
+    const bool real = tok < it.ntok;  // (the same for the whole warp)
     const bool whole = it.whole();
     const int slot = 2 * g + (it.blk0 == 0 ? 1 : 0);
-    const float inv = v_mul / l;
-    uint16_t* out = a.out + (static_cast<size_t>(it.row0 + tok) * kHeads + head) * kHeadDim + 128 * half;
-    float* acc = slot_acc(a.partials, slot) + (rank * kRows + row) * kHeadDim + 128 * half;
+    if (whole) {
+      // 64 dimensions at a time: rounded, then exchanged among groups of eight lanes so that a
+      // store covers whole 128-byte lines of four rows (a store of each lane's own row
+      // touched 32 lines, and the epilogue took 12000 cycles instead of 2500)
+      const float inv = v_mul / l;
+      uint16_t* out = a.out + (static_cast<size_t>(it.row0 + tok) * kHeads + (head & ~7)) * kHeadDim +
+                      128 * half + 8 * (lane & 7);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tmem + lane_addr + kTmemO + 128 * half + 32 * c, r);
-      tmem_wait_ld();
-      if (c == 3) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) remote_arrive(o_bar);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r0[32], r1[32], w[32];
+        tmem_ld_32x32b_x32(o_addr + 64 * c, r0);
+        tmem_ld_32x32b_x32(o_addr + 64 * c + 32, r1);
+        tmem_wait_ld();
+        if (c == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(o_bar);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          w[i] = pack_bf16x2(__uint_as_float(r0[2 * i]) * inv, __uint_as_float(r0[2 * i + 1]) * inv);
+          w[16 + i] = pack_bf16x2(__uint_as_float(r1[2 * i]) * inv, __uint_as_float(r1[2 * i + 1]) * inv);
+        }
+        transpose_pieces(w, lane);
+        if (ok && real) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(out + j * kHeadDim + 64 * c) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
       }
-      float o[32];
+    } else {
+      // partials: [4 dimensions][row] so that a store is 512 bytes of consecutive rows
+      float* acc = slot_acc(a.partials, slot) + (32 * half * kChunkRows + rank * kRows + row) * 4;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(o_addr + 32 * c, r);
+        tmem_wait_ld();
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(o_bar);
+        }
+        if (ok && real) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
-      if (bad != 0) add_late<kFp8>(a, it, late, bad, tok, 128 * half + 32 * c, o);
-      if (!ok || !real) continue;
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
-              make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                         pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(acc + 32 * c + 4 * i) =
-              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(acc + (8 * c + i) * kChunkRows * 4) =
+                make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        }
       }
     }
     if (!whole) {
@@ -1083,8 +1214,13 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
         info = make_int2(it.row0, (last - g + 1) * 8 + it.ntok);
       }
     }
-    // (the next item writes xch only behind this pair's next barrier)
-    named_bar_sync(bar, 64);
+    if (bad != 0) {
+      // the flag is spent: back to 0 once both halves' warps of this CTA have read it
+      named_bar_sync(5 + half, 32 * kSoftmaxWarps / 2);
+      if (st % 128 == 0) S.bad[item & 1][half] = 0;
+    }
+    // (FP8: the next item's Q split writes xch)
+    if constexpr (kFp8) named_bar_sync(bar, 64);
     ++item;
   }
   if (rank == 0 && st == 0) a.info[g] = info;
@@ -1116,6 +1252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&S.o_free, 2 * kSoftmaxWarps);
     mbar_init(&S.mma_done, 1);
+    S.bad[0][0] = S.bad[0][1] = S.bad[1][0] = S.bad[1][1] = 0;
     S.abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&q_map);
@@ -1151,42 +1288,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// merge of the tiles that several pairs share: one warp a row, fixed order
+// merge of the tiles that several pairs share, in a fixed order. A block takes 32 rows and 64
+// dimensions of one tile: lane = row, warp = 16 of the dimensions.
 // ---------------------------------------------------------------------------------------
 constexpr int kCombineWarps = 4;
+constexpr int kCombineRows = 32, kCombineDims = 16 * kCombineWarps;
 
 __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(ChunkAttnArgs a) {
+  __shared__ __align__(16) uint4 tile[kCombineRows][kCombineDims / 8 + 1];
   pdl_launch_dependents();
   pdl_wait();
-  const int g = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);  // of the tile's 256
+  const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int2 info = __ldcg(&a.info[g]);
   const int parts = info.y >> 3, ntok = info.y & 7;
-  if (row >= ntok * kHeads) return;
+  const int row0 = blockIdx.y * kCombineRows, row = row0 + lane;
+  const int dim0 = blockIdx.z * kCombineDims;
+  if (row0 >= ntok * kHeads) return;
   // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
   auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
   float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(slot_m(a.partials, slot(i)) + row));
-  M = warp_max_f32(M);
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[8] = {};
-#pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const float* acc = slot_acc(a.partials, slot(i)) + row * kHeadDim + 8 * lane;
+    const float m = __ldcg(slot_m(a.partials, slot(i)) + row);
+    M = max3(M, m, m);
+  }
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, o[16] = {};
+#pragma unroll 2
+  for (int i = 0; i < parts; ++i) {
+    const float* acc = slot_acc(a.partials, slot(i)) + ((dim0 / 4 + 4 * warp) * kChunkRows + row) * 4;
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = __ldcg(reinterpret_cast<const float4*>(acc + k * kChunkRows * 4));
     const float w = ex2(__ldcg(slot_m(a.partials, slot(i)) + row) - base);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(acc));
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(acc + 4));
     L = fmaf(w, __ldcg(slot_l(a.partials, slot(i)) + row), L);
-    o[0] = fmaf(w, x.x, o[0]), o[1] = fmaf(w, x.y, o[1]);
-    o[2] = fmaf(w, x.z, o[2]), o[3] = fmaf(w, x.w, o[3]);
-    o[4] = fmaf(w, y.x, o[4]), o[5] = fmaf(w, y.y, o[5]);
-    o[6] = fmaf(w, y.z, o[6]), o[7] = fmaf(w, y.w, o[7]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[4 * k] = fmaf(w, x[k].x, o[4 * k]);
+      o[4 * k + 1] = fmaf(w, x[k].y, o[4 * k + 1]);
+      o[4 * k + 2] = fmaf(w, x[k].z, o[4 * k + 2]);
+      o[4 * k + 3] = fmaf(w, x[k].w, o[4 * k + 3]);
+    }
   }
   const float inv = (a.kv_dtype == MFA_KV_FP8_E4M3 ? a.v_scale : 1.f) / L;
-  uint16_t* out = a.out + (static_cast<size_t>(info.x) * kHeads + row) * kHeadDim + 8 * lane;
-  *reinterpret_cast<uint4*>(out) =
-      make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                 pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    tile[lane][2 * warp + k] = make_uint4(
+        pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+        pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+  __syncthreads();
+  // whole 128-byte lines of the rows
+  for (int i = threadIdx.x; i < kCombineRows * (kCombineDims / 8); i += 32 * kCombineWarps) {
+    const int r = i / (kCombineDims / 8), piece = i % (kCombineDims / 8);
+    *reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(info.x) * kHeads + row0 + r) * kHeadDim + dim0 +
+                              8 * piece) = tile[r][piece];
+  }
 }
 
 using Kernel = void (*)(CUtensorMap, ChunkAttnArgs);
@@ -1231,7 +1387,8 @@ cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const ChunkAttnArgs& a, 
   const cudaError_t e =
       launch_pdl(kernel, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, q_map, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_combine_kernel, dim3(a.pairs, kChunkRows / kCombineWarps),
+  return launch_pdl(chunk_combine_kernel,
+                    dim3(a.pairs, kChunkRows / kCombineRows, kHeadDim / kCombineDims),
                     dim3(32 * kCombineWarps), 0, s, a);
 }
 
