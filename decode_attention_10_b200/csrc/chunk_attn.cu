@@ -63,9 +63,11 @@ constexpr int kSlots = 9;
 constexpr int kBoxBytes = kChunkBoxRows * 128;  // [64 rows x 128 bytes]
 constexpr int kQChunkBytes = kRows * 128;       // [128 rows x 128 bytes]
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 64 + 32 * kSoftmaxWarps;
+constexpr int kHelperWarp = 2 + kSoftmaxWarps;
+constexpr int kThreads = 32 * (kHelperWarp + 1);
+constexpr int kStageSlots = 4;  // ring slots that a finished tile's 128 x 256 bf16 results take
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
-constexpr int kTileCost = 1;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
+constexpr int kTileCost = 2;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
@@ -90,13 +92,20 @@ struct __align__(1024) Smem {
   uint8_t ring[kSlots * kSlotBytes];
   Plan plan;
   float xch[2][kRows];        // exchange between the two threads of a row
-  uint64_t kv_full[kSlots];   // first CTA: both halves of a slot have landed
+  uint64_t kv_full[kSlots];   // first CTA: both halves of a slot have landed (and are clean)
   uint64_t kv_empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2];
-  uint64_t v_full[kSlots];    // this CTA: a slot's V half of a special block has landed
+  // this CTA: the V half of its i-th special block has landed, by i modulo kSlots. (Not by the
+  // slot: only the helper warp waits for these, and it may be several uses of a slot behind
+  // the producer or ahead of it. Special block i + kSlots cannot be loaded before block i is
+  // used up, and the helper sees every one of them.)
+  uint64_t v_full[kSlots];
   uint64_t pv_done[2];        // by the block's parity: a waiter is at most one block behind
   uint64_t o_free;
+  uint64_t stage_free;        // the ring slots for a tile's results are free
+  uint64_t staged;            // this CTA's results of a tile are in them
+  uint64_t stored;            // first CTA: the other CTA's have left it
   uint64_t mma_done;
   uint32_t bad[2][2];         // [item parity][V half]: late rows held out of the product
   uint32_t tmem_base;
@@ -147,6 +156,10 @@ __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void remote_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void remote_arrive_release(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
@@ -178,6 +191,21 @@ __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, 
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// A box of shared memory to a tensor in global memory.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+// Wait until the stores that this thread has issued have read their shared memory.
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem) {
@@ -473,7 +501,7 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
   const uint32_t q_bar = map_to(&S.q_full, 0);
   const int page_shift = kPaged ? 31 - __clz(a.page_size) : 0;
-  uint32_t chunk = 0, issued = 0;
+  uint32_t chunk = 0, issued = 0, specials = 0;
   int item = 0;
   Cursor cur;
   cur.init(S.plan, a.batch, g, G);
@@ -521,41 +549,46 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
         }
       }
     };
-    // the next slot of the ring, free, and the barrier that its bytes complete on: the pair's,
-    // or (local) this CTA's. Both barriers see a phase per use of the slot.
-    auto take = [&](bool local, uint32_t& bar) {
-      const uint32_t slot = chunk % kSlots, use = chunk / kSlots;
+    // The next slot of the ring, free. Each use of a slot is a phase of the pair's barrier, with
+    // an arrival for each CTA: its producer's here, or for a special block's V that of its
+    // helper, once it has looked the values over.
+    auto take = [&](uint32_t& slot) {
+      slot = chunk % kSlots;
+      const uint32_t use = chunk / kSlots;
       if (use > 0) mbar_wait(&S.kv_empty[slot], (use - 1) & 1, abort);
-      if (leader && !*abort) {
-        if (local) {
-          mbar_arrive_expect_tx(&S.v_full[slot], kSlotBytes);
-          if (rank == 0) mbar_arrive(&S.kv_full[slot]);
-        } else {
-          mbar_arrive(&S.v_full[slot]);
-          if (rank == 0) mbar_arrive_expect_tx(&S.kv_full[slot], 2 * kSlotBytes);
-        }
-        issued = chunk + 1;
-      }
-      bar = local ? smem_u32(&S.v_full[slot]) : map_to(&S.kv_full[slot], 0);
       ++chunk;
-      return S.ring + slot * kSlotBytes;
+      return map_to(&S.kv_full[slot], 0);
     };
     auto load_k = [&](int blk) {
-      uint32_t bar;
       // this CTA's 64 keys, all dimensions
       for (int c = 0; c < C::kKSlots; ++c) {
-        uint8_t* dst = take(false, bar);
-        load(dst, &map->k, kg, 2 * blk + rank, c * 128, 2, bar);
+        uint32_t slot;
+        const uint32_t bar = take(slot);
+        if (leader && !*abort) {
+          remote_arrive_expect_tx(bar, kSlotBytes);
+          issued = chunk;
+        }
+        load(S.ring + slot * kSlotBytes, &map->k, kg, 2 * blk + rank, c * 128, 2, bar);
       }
     };
     auto load_v = [&](int blk) {
-      // all keys, this CTA's 128 dimensions. Special blocks land on this CTA's own barrier:
-      // its softmax warps look them over before the product may read them.
-      const bool local = blk >= it.special();
+      // all keys, this CTA's 128 dimensions. Special blocks land on a barrier of this CTA's own,
+      // where its helper warp waits for them.
+      const bool special = blk >= it.special();
       const int x = 128 * rank;
-      uint32_t bar;
+      uint64_t* own = &S.v_full[specials % kSlots];
       for (int c = 0; c < C::kVSlots; ++c) {
-        uint8_t* dst = take(local, bar);
+        uint32_t slot;
+        uint32_t bar = take(slot);
+        if (leader && !*abort) {
+          if (!special)
+            remote_arrive_expect_tx(bar, kSlotBytes);
+          else if (c == 0)
+            mbar_arrive_expect_tx(own, C::kVSlots * kSlotBytes);
+          issued = chunk;
+        }
+        if (special) bar = smem_u32(own);
+        uint8_t* dst = S.ring + slot * kSlotBytes;
         if constexpr (kFp8) {
           load(dst, &map->v, vg, 2 * blk, x, 1, bar);
           load(dst + kBoxBytes, &map->v, vg, 2 * blk + 1, x, 1, bar);
@@ -563,20 +596,31 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
           load(dst, &map->v, vg, 2 * blk + c, x, 2, bar);
         }
       }
+      specials += special;
     };
     load_k(it.blk0);
     for (int blk = it.blk0; blk < it.blk1; ++blk) {
       if (blk + 1 < it.blk1) load_k(blk + 1);
       load_v(blk);
     }
+    if (it.whole()) {
+      for (int c = 0; c < kStageSlots; ++c) {
+        uint32_t slot;
+        const uint32_t bar = take(slot);
+        if (leader && !*abort) remote_arrive(bar);
+      }
+      if (leader && !*abort) mbar_arrive(&S.stage_free);
+    }
     ++item;
   }
-  // Before the CTAs may exit, every copy must have landed (after an abort; else all were used).
+  // Before the CTAs may exit, every copy must have landed (after an abort; else all were used):
+  // those of both CTAs that the pair's barriers count are waited for in the first.
   if (*abort && leader) {
-    for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c) {
-      if (rank == 0) mbar_wait_drain(&S.kv_full[c % kSlots], (c / kSlots) & 1);
+    if (rank == 0)
+      for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c)
+        mbar_wait_drain(&S.kv_full[c % kSlots], (c / kSlots) & 1);
+    for (uint32_t c = specials > kSlots ? specials - kSlots : 0; c < specials; ++c)
       mbar_wait_drain(&S.v_full[c % kSlots], (c / kSlots) & 1);
-    }
     if (!kFp8 && rank == 0 && item > 0) mbar_wait_drain(&S.q_full, (item - 1) & 1);
   }
   __syncwarp();
@@ -674,6 +718,7 @@ __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t 
       if (t + 1 == n && !kFp8 && leader && !*abort) pair_commit(&S.q_empty);
       issue_pv(gt + t, t == 0);
     }
+    if (it.whole()) chunk += kStageSlots;
     gt += n;
     ++item;
   }
@@ -840,48 +885,45 @@ __device__ __noinline__ int split_q(Smem& S, const ChunkAttnArgs& a, const Item&
   return e;
 }
 
-// A special block's V half in this CTA's ring, by the 256 softmax threads (st): rows of keys
-// that no token of the tile sees are zeroed; by warp 0 of them, rows that only its later
-// tokens see (key p0 + 1 + i, i < ntok - 1) are zeroed too if they hold an infinity or NaN,
-// and their bits i returned (on warp 0).
+// A special block's V half in this CTA's ring (its first slot's use `chunk`), by one warp: rows
+// of keys that no token of the tile sees are zeroed; rows that only its later tokens see (key
+// p0 + 1 + i, i < ntok - 1) are zeroed too if they hold an infinity or NaN, and their bits i
+// returned.
 template <bool kFp8>
-__device__ __noinline__ uint32_t clean_v(Smem& S, const Item& it, int blk, uint32_t chunk,
-                                         int st) {
-  constexpr int kDc = kFp8 ? 1 : 2;  // boxes across this CTA's 128 dimensions
-  auto row_piece = [&](int r, int piece) {  // 16-byte piece of key r of the block
-    const int kh = r / kChunkBoxRows;
-    const uint32_t slot = (chunk + (kFp8 ? 0 : kh)) % kSlots;
-    uint8_t* box = S.ring + slot * kSlotBytes + (kFp8 ? kh * kBoxBytes : (piece / 8) * kBoxBytes);
-    return reinterpret_cast<uint4*>(box + (r % kChunkBoxRows) * 128 + (piece % 8) * 16);
+__device__ __forceinline__ uint32_t clean_v(Smem& S, const Item& it, int blk, uint32_t chunk,
+                                            int lane) {
+  constexpr int kPieces = kFp8 ? 8 : 16;  // 16-byte pieces of a key's 128 dimensions
+  uint8_t* slot0 = S.ring + (chunk % kSlots) * kSlotBytes;
+  uint8_t* slot1 = kFp8 ? slot0 + kBoxBytes : S.ring + ((chunk + 1) % kSlots) * kSlotBytes;
+  // keys 64 h .. 64 h + 63 of the block are rows of 128 bytes from here on (bf16: two boxes)
+  auto row_piece = [&](int r, int piece) {
+    uint8_t* half = r < kChunkBoxRows ? slot0 : slot1;
+    return reinterpret_cast<uint4*>(half + (piece / 8) * kBoxBytes + (r % kChunkBoxRows) * 128 +
+                                    (piece % 8) * 16);
   };
   const int from = max(0, it.kend() - blk * kBlock);
-  const int n = (kBlock - from) * 8 * kDc;
-  for (int i = st; i < n; i += 32 * kSoftmaxWarps)
-    *row_piece(from + i / (8 * kDc), i % (8 * kDc)) = make_uint4(0, 0, 0, 0);
+  for (int r = from + lane / kPieces; r < kBlock; r += 32 / kPieces)
+    *row_piece(r, lane % kPieces) = make_uint4(0, 0, 0, 0);
   uint32_t bad = 0;
-  if (st < 32) {
-    for (int i = 0; i + 1 < it.ntok; ++i) {
-      const int r = it.p0 + 1 + i - blk * kBlock;
-      if (r < 0 || r >= kBlock) continue;
-      bool odd = false;
-      if (st < 8 * kDc) {
-        const uint4 v = *row_piece(r, st);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (kFp8) {
-            // a byte of 0x7F or 0xFF
-            const uint32_t y = (w[k] & 0x7F7F7F7Fu) + 0x01010101u;
-            odd |= (y & 0x80808080u) != 0;
-          } else {
-            odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
-          }
-        }
+  for (int i = 0; i < kTokens - 1; ++i) {
+    const int r = it.p0 + 1 + i - blk * kBlock;
+    if (i + 1 >= it.ntok || r < 0 || r >= kBlock) continue;
+    bool odd = false;
+    if (lane < kPieces) {
+      const uint4 v = *row_piece(r, lane);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (kFp8)  // a byte of 0x7F or 0xFF
+          odd |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        else
+          odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
       }
-      if (__any_sync(0xffffffffu, odd)) {
-        bad |= 1u << i;
-        if (st < 8 * kDc) *row_piece(r, st) = make_uint4(0, 0, 0, 0);
-      }
+    }
+    if (__any_sync(0xffffffffu, odd)) {
+      bad |= 1u << i;
+      if (lane < kPieces) *row_piece(r, lane) = make_uint4(0, 0, 0, 0);
     }
   }
   return bad;
@@ -939,26 +981,6 @@ __device__ __noinline__ void add_late(const ChunkAttnArgs& a, const Item& it, ui
   tmem_wait_st();
 }
 
-// 16-byte pieces: lane i of a group of eight has piece j of its own row in w[4 j ..]; after it,
-// piece i of row j of the group there.
-__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[32], int lane) {
-#pragma unroll
-  for (int d = 4; d > 0; d >>= 1) {
-    const bool up = lane & d;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j & d) continue;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t& x = w[4 * j + k];
-        uint32_t& y = w[4 * (j | d) + k];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x : y, d);
-        (up ? x : y) = got;
-      }
-    }
-  }
-}
-
 template <bool kFp8>
 __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t rank,
                             uint32_t tmem) {
@@ -978,7 +1000,7 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
   const uint32_t o_bar = map_to(&S.o_free, 0);
   const uint32_t q_bar = map_to(&S.q_full, 0);
   uint32_t gt = 0, chunk = 0;
-  int item = 0;
+  int item = 0, tiles = 0;
 
   // rows of refused sequences
   for (int b = g; b < a.batch; b += gridDim.x / 2) {
@@ -1008,7 +1030,6 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     float m = -INFINITY, base = 0.f, l = 0.f;  // m: raw; base = m mul (0 while m is -inf)
     const float thr_step = C::kRescale / mul;
     float thr = -INFINITY;
-    uint32_t bad_mine = 0;
 
     for (int t = 0; t < n; ++t) {
       const uint32_t j = (gt + t) & 1;
@@ -1112,26 +1133,9 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
         tmem_st_32x32b_x32(sa + 32 * half, pw);
       }
       tmem_wait_st();
-      if (special) {
-        // the V half of this block, before the product may read it
-        const uint32_t vc = chunk + C::kKSlots + t * (C::kKSlots + C::kVSlots) +
-                            (t + 1 < n ? C::kKSlots : 0);
-#pragma unroll
-        for (int c = 0; c < C::kVSlots; ++c)
-          mbar_wait(&S.v_full[(vc + c) % kSlots], ((vc + c) / kSlots) & 1, abort);
-        if (!*abort) bad_mine |= clean_v<kFp8>(S, it, blk, vc, st);
-        if (bad_mine != 0 && lane < 2)  // (warp 0) for the epilogues of both CTAs
-          remote_store(map_to(&S.bad[item & 1][rank], lane), bad_mine);
-        fence_proxy_async_smem();
-      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (bad_mine != 0)
-          remote_arrive_release(p_bar[j]);
-        else
-          remote_arrive(p_bar[j]);
-      }
+      if (lane == 0) remote_arrive(p_bar[j]);
     }
     gt += n;
     chunk += n * (C::kKSlots + C::kVSlots);
@@ -1151,36 +1155,37 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     const bool whole = it.whole();
     const int slot = 2 * g + (it.blk0 == 0 ? 1 : 0);
     if (whole) {
-      // 64 dimensions at a time: rounded, then exchanged among groups of eight lanes so that a
-      // store covers whole 128-byte lines of four rows (a store of each lane's own row
-      // touched 32 lines, and the epilogue took 12000 cycles instead of 2500)
+      // rounded into the ring, as boxes of [128 rows x 64 dimensions] with 128-byte swizzle,
+      // for the helper warp to store (stores of each lane's own row touch 32 lines each: the
+      // epilogue took 12000 cycles that way, 3300 after a transposition by shuffles, 1000 so)
       const float inv = v_mul / l;
-      uint16_t* out = a.out + (static_cast<size_t>(it.row0 + tok) * kHeads + (head & ~7)) * kHeadDim +
-                      128 * half + 8 * (lane & 7);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t r0[32], r1[32], w[32];
-        tmem_ld_32x32b_x32(o_addr + 64 * c, r0);
-        tmem_ld_32x32b_x32(o_addr + 64 * c + 32, r1);
+      mbar_wait(&S.stage_free, tiles & 1, abort);
+      ++tiles;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(o_addr + 32 * c, r);
         tmem_wait_ld();
-        if (c == 1) {
+        if (c == 3) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) remote_arrive(o_bar);
         }
+        uint8_t* dst = S.ring + ((chunk + 2 * half + c / 2) % kSlots) * kSlotBytes + row * 128;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          w[i] = pack_bf16x2(__uint_as_float(r0[2 * i]) * inv, __uint_as_float(r0[2 * i + 1]) * inv);
-          w[16 + i] = pack_bf16x2(__uint_as_float(r1[2 * i]) * inv, __uint_as_float(r1[2 * i + 1]) * inv);
-        }
-        transpose_pieces(w, lane);
-        if (ok && real) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(out + j * kHeadDim + 64 * c) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        for (int i = 0; i < 4; ++i) {
+          const int piece = 4 * (c & 1) + i;
+          *reinterpret_cast<uint4*>(dst + ((piece ^ (row & 7)) << 4)) = make_uint4(
+              pack_bf16x2(__uint_as_float(r[8 * i]) * inv, __uint_as_float(r[8 * i + 1]) * inv),
+              pack_bf16x2(__uint_as_float(r[8 * i + 2]) * inv, __uint_as_float(r[8 * i + 3]) * inv),
+              pack_bf16x2(__uint_as_float(r[8 * i + 4]) * inv, __uint_as_float(r[8 * i + 5]) * inv),
+              pack_bf16x2(__uint_as_float(r[8 * i + 6]) * inv, __uint_as_float(r[8 * i + 7]) * inv));
         }
       }
+      chunk += kStageSlots;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.staged);
     } else {
       // partials: [4 dimensions][row] so that a store is 512 bytes of consecutive rows
       float* acc = slot_acc(a.partials, slot) + (32 * half * kChunkRows + rank * kRows + row) * 4;
@@ -1226,9 +1231,90 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
   if (rank == 0 && st == 0) a.info[g] = info;
 }
 
+// ---------------------------------------------------------------------------------------
+// the helper warp: looks special blocks' V over, stores finished tiles
+// ---------------------------------------------------------------------------------------
+template <bool kFp8>
+__device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnArgs& a, int g, int G,
+                           uint32_t rank) {
+  using C = Cfg<kFp8>;
+  volatile int* abort = &S.abort_flag;
+  const int lane = threadIdx.x & 31;
+  const bool leader = elect_one();
+  const uint32_t stored_bar = map_to(&S.stored, 0);
+  uint32_t chunk = 0, specials = 0;
+  int item = 0, tiles = 0;
+  Cursor cur;
+  cur.init(S.plan, a.batch, g, G);
+  Item it;
+  while (cur.next(it)) {
+    const int n = it.blk1 - it.blk0;
+    uint32_t bad = 0;
+    for (int blk = max(it.blk0, it.special()); blk < it.blk1; ++blk) {
+      const int t = blk - it.blk0;
+      // the use of V's first slot: K of blocks 0 .. t + 1 and V of 0 .. t - 1 come before it
+      const uint32_t vc = chunk + C::kKSlots + t * (C::kKSlots + C::kVSlots) +
+                          (t + 1 < n ? C::kKSlots : 0);
+      mbar_wait(&S.v_full[specials % kSlots], (specials / kSlots) & 1, abort);
+      ++specials;
+      if (__shfl_sync(0xffffffffu, *abort, 0) != 0) break;
+      bad |= clean_v<kFp8>(S, it, blk, vc, lane);
+      if (bad != 0 && lane < 2)  // for the epilogues of both CTAs
+        remote_store(map_to(&S.bad[item & 1][rank], lane), bad);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (leader) {
+#pragma unroll
+        for (int c = 0; c < C::kVSlots; ++c) {
+          const uint32_t bar = map_to(&S.kv_full[(vc + c) % kSlots], 0);
+          if (bad != 0)
+            remote_arrive_release(bar);
+          else
+            remote_arrive(bar);
+        }
+      }
+      __syncwarp();
+    }
+    chunk += n * (C::kKSlots + C::kVSlots);
+    if (it.whole()) {
+      mbar_wait(&S.staged, tiles & 1, abort);
+      if (leader && !*abort) {
+        for (int k = 0; k < kCtaTokens; ++k) {
+          const int tok = kCtaTokens * rank + k;
+          if (tok >= it.ntok) break;
+          for (int c = 0; c < kStageSlots; ++c)
+            tma_store_2d(out_map, 64 * c, (it.row0 + tok) * kHeads,
+                         S.ring + ((chunk + c) % kSlots) * kSlotBytes + k * kHeads * 128);
+        }
+        tma_store_wait_read();
+        // the slots are free in both CTAs at once: a slot's next use counts an arrival of each
+        // CTA on the pair's barrier, so neither may be a use ahead
+        if (rank != 0) remote_arrive(stored_bar);
+      }
+      __syncwarp();
+      if (rank == 0) {
+        mbar_wait(&S.stored, tiles & 1, abort);
+        if (leader && !*abort) {
+          for (int c = 0; c < kStageSlots; ++c) {
+            uint64_t* e = &S.kv_empty[(chunk + c) % kSlots];
+            mbar_arrive(e);
+            remote_arrive(map_to(e, 1));
+          }
+        }
+      }
+      chunk += kStageSlots;
+      ++tiles;
+    }
+    ++item;
+  }
+  if (leader) tma_store_wait_done();
+  __syncwarp();
+}
+
 template <bool kFp8, bool kPaged>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ CUtensorMap out_map,
                       const __grid_constant__ ChunkAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1239,7 +1325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&S.kv_full[i], 1);
+      mbar_init(&S.kv_full[i], 2);
       mbar_init(&S.kv_empty[i], 1);
       mbar_init(&S.v_full[i], 1);
     }
@@ -1251,11 +1337,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[i], 2 * kSoftmaxWarps);
     }
     mbar_init(&S.o_free, 2 * kSoftmaxWarps);
+    mbar_init(&S.stage_free, 1);
+    mbar_init(&S.staged, kSoftmaxWarps);
+    mbar_init(&S.stored, 1);
     mbar_init(&S.mma_done, 1);
     S.bad[0][0] = S.bad[0][1] = S.bad[1][0] = S.bad[1][1] = 0;
     S.abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&q_map);
+    prefetch_tensormap(&out_map);
   }
   if (warp == 1) pair_tmem_alloc(&S.tmem_base);
   pdl_launch_dependents();
@@ -1271,6 +1361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     run_producer<kFp8, kPaged>(S, &q_map, a, g, G, rank);
   } else if (warp == 1) {
     if (rank == 0) run_mma<kFp8>(S, a, g, G, tmem);
+  } else if (warp == kHelperWarp) {
+    run_helper<kFp8>(S, &out_map, a, g, G, rank);
   } else {
     run_softmax<kFp8>(S, a, g, G, rank, tmem);
   }
@@ -1278,6 +1370,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && S.abort_flag) atomicOr(a.err, kErrTimeout);
+  // the last commit of the products reaches both CTAs: neither may be gone by then
+  if (warp == 1 && rank != 0) mbar_wait_drain(&S.mma_done, 0);
   __syncwarp();
   cluster_sync();  // the other CTA's products and arrivals are done with this one's memory
   tc_fence_after();
@@ -1345,7 +1439,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(Chunk
   }
 }
 
-using Kernel = void (*)(CUtensorMap, ChunkAttnArgs);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, ChunkAttnArgs);
 constexpr int kSmemBytes = sizeof(Smem) + 1024;
 
 // The kernel of a call's cache type and layout, its shared-memory limit raised; null on error.
@@ -1381,11 +1475,12 @@ int chunk_attn_pairs(const ChunkAttnArgs& a) {
   return n;
 }
 
-cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const ChunkAttnArgs& a, cudaStream_t s) {
+cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const CUtensorMap& out_map,
+                              const ChunkAttnArgs& a, cudaStream_t s) {
   const Kernel kernel = kernel_of(a);
   if (kernel == nullptr) return cudaErrorInvalidValue;
   const cudaError_t e =
-      launch_pdl(kernel, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, q_map, a);
+      launch_pdl(kernel, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, q_map, out_map, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_combine_kernel,
                     dim3(a.pairs, kChunkRows / kCombineRows, kHeadDim / kCombineDims),
