@@ -105,7 +105,6 @@ struct __align__(1024) Smem {
   uint64_t o_free;
   uint64_t stage_free;        // the ring slots for a tile's results are free
   uint64_t staged;            // this CTA's results of a tile are in them
-  uint64_t stored;            // first CTA: the other CTA's have left it
   uint64_t mma_done;
   uint32_t bad[2][2];         // [item parity][V half]: late rows held out of the product
   uint32_t tmem_base;
@@ -200,9 +199,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
                "r"(x), "r"(y), "r"(smem_u32(src))
                : "memory");
 }
-// Wait until the stores that this thread has issued have read their shared memory.
+__device__ __forceinline__ void tma_store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Wait until all but the last N groups of stores of this thread have read their shared memory.
+template <int N>
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void tma_store_wait_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -716,6 +719,14 @@ __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t 
     for (int t = 0; t < n; ++t) {
       if (t + 1 < n) issue_s(gt + t + 1);
       if (t + 1 == n && !kFp8 && leader && !*abort) pair_commit(&S.q_empty);
+      if (t + 1 == n && it.whole()) {
+        // both producers have counted the uses of the slots behind V that take the results, so
+        // that a CTA which is done with them early cannot count its next use into this one
+        for (int c = 0; c < kStageSlots; ++c) {
+          const uint32_t sc = chunk + C::kVSlots + c;
+          mbar_wait(&S.kv_full[sc % kSlots], (sc / kSlots) & 1, abort);
+        }
+      }
       issue_pv(gt + t, t == 0);
     }
     if (it.whole()) chunk += kStageSlots;
@@ -1047,10 +1058,17 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
 #pragma unroll
         for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r0[i]), s[32 + i] = __uint_as_float(r1[i]);
       }
-      const int left = lim - (blk * kBlock + 64 * half);  // of these 64 keys, those below it
       if (special) {
+        // of these 64 keys those below lim are seen (the same number in the whole warp); eight
+        // at a time, so that only the eight that lim falls into are compared one by one
+        const int left = lim - (blk * kBlock + 64 * half);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : -INFINITY;
+        for (int e = 0; e < 64; e += 8) {
+          if (left < e + 8) {
+#pragma unroll
+            for (int i = e; i < e + 8; ++i) s[i] = i < left ? s[i] : -INFINITY;
+          }
+        }
       }
       float mx = max3(s[0], s[1], s[2]);
       {
@@ -1162,24 +1180,25 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
       mbar_wait(&S.stage_free, tiles & 1, abort);
       ++tiles;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(o_addr + 32 * c, r);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[2][32];
+        tmem_ld_32x32b_x32(o_addr + 64 * c, r[0]);
+        tmem_ld_32x32b_x32(o_addr + 64 * c + 32, r[1]);
         tmem_wait_ld();
-        if (c == 3) {
+        if (c == 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) remote_arrive(o_bar);
         }
-        uint8_t* dst = S.ring + ((chunk + 2 * half + c / 2) % kSlots) * kSlotBytes + row * 128;
+        uint8_t* dst = S.ring + ((chunk + 2 * half + c) % kSlots) * kSlotBytes + row * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int piece = 4 * (c & 1) + i;
+        for (int piece = 0; piece < 8; ++piece) {
+          const uint32_t* v = r[piece / 4] + 8 * (piece % 4);
           *reinterpret_cast<uint4*>(dst + ((piece ^ (row & 7)) << 4)) = make_uint4(
-              pack_bf16x2(__uint_as_float(r[8 * i]) * inv, __uint_as_float(r[8 * i + 1]) * inv),
-              pack_bf16x2(__uint_as_float(r[8 * i + 2]) * inv, __uint_as_float(r[8 * i + 3]) * inv),
-              pack_bf16x2(__uint_as_float(r[8 * i + 4]) * inv, __uint_as_float(r[8 * i + 5]) * inv),
-              pack_bf16x2(__uint_as_float(r[8 * i + 6]) * inv, __uint_as_float(r[8 * i + 7]) * inv));
+              pack_bf16x2(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv),
+              pack_bf16x2(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv),
+              pack_bf16x2(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv),
+              pack_bf16x2(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv));
         }
       }
       chunk += kStageSlots;
@@ -1241,7 +1260,6 @@ __device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnA
   volatile int* abort = &S.abort_flag;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
-  const uint32_t stored_bar = map_to(&S.stored, 0);
   uint32_t chunk = 0, specials = 0;
   int item = 0, tiles = 0;
   Cursor cur;
@@ -1279,29 +1297,25 @@ __device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnA
     if (it.whole()) {
       mbar_wait(&S.staged, tiles & 1, abort);
       if (leader && !*abort) {
-        for (int k = 0; k < kCtaTokens; ++k) {
-          const int tok = kCtaTokens * rank + k;
-          if (tok >= it.ntok) break;
-          for (int c = 0; c < kStageSlots; ++c)
-            tma_store_2d(out_map, 64 * c, (it.row0 + tok) * kHeads,
+        const int rows = min(kCtaTokens, it.ntok - kCtaTokens * static_cast<int>(rank));
+        for (int c = 0; c < kStageSlots; ++c) {
+          for (int k = 0; k < rows; ++k)
+            tma_store_2d(out_map, 64 * c, (it.row0 + kCtaTokens * rank + k) * kHeads,
                          S.ring + ((chunk + c) % kSlots) * kSlotBytes + k * kHeads * 128);
+          tma_store_commit();
         }
-        tma_store_wait_read();
-        // the slots are free in both CTAs at once: a slot's next use counts an arrival of each
-        // CTA on the pair's barrier, so neither may be a use ahead
-        if (rank != 0) remote_arrive(stored_bar);
+        // each slot is free once its store has read it
+        tma_store_wait_read<3>();
+        mbar_arrive(&S.kv_empty[chunk % kSlots]);
+        tma_store_wait_read<2>();
+        mbar_arrive(&S.kv_empty[(chunk + 1) % kSlots]);
+        tma_store_wait_read<1>();
+        mbar_arrive(&S.kv_empty[(chunk + 2) % kSlots]);
+        tma_store_wait_read<0>();
+        mbar_arrive(&S.kv_empty[(chunk + 3) % kSlots]);
+        static_assert(kStageSlots == 4, "the waits above");
       }
       __syncwarp();
-      if (rank == 0) {
-        mbar_wait(&S.stored, tiles & 1, abort);
-        if (leader && !*abort) {
-          for (int c = 0; c < kStageSlots; ++c) {
-            uint64_t* e = &S.kv_empty[(chunk + c) % kSlots];
-            mbar_arrive(e);
-            remote_arrive(map_to(e, 1));
-          }
-        }
-      }
       chunk += kStageSlots;
       ++tiles;
     }
@@ -1339,7 +1353,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&S.o_free, 2 * kSoftmaxWarps);
     mbar_init(&S.stage_free, 1);
     mbar_init(&S.staged, kSoftmaxWarps);
-    mbar_init(&S.stored, 1);
     mbar_init(&S.mma_done, 1);
     S.bad[0][0] = S.bad[0][1] = S.bad[1][0] = S.bad[1][1] = 0;
     S.abort_flag = 0;
