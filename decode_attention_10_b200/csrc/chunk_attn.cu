@@ -85,6 +85,8 @@ struct Plan {
   int32_t cost[kMaxBatch + 1];   // exclusive prefix of the sequences' costs
   int32_t start[kMaxBatch + 1];  // q_start
   int32_t len[kMaxBatch];        // seq_lens; -1: refused
+  const int32_t* pages;          // paged: the page table, `page_stride` entries a sequence
+  int32_t page_stride;
 };
 
 struct __align__(1024) Smem {
@@ -92,6 +94,7 @@ struct __align__(1024) Smem {
   uint8_t ring[kSlots * kSlotBytes];
   Plan plan;
   float xch[2][kRows];        // exchange between the two threads of a row
+  int32_t q_exp[kRows];       // FP8: exponent of each row's scale of Q
   uint64_t kv_full[kSlots];   // first CTA: both halves of a slot have landed (and are clean)
   uint64_t kv_empty[kSlots];
   uint64_t q_full, q_empty;
@@ -122,9 +125,11 @@ __device__ __forceinline__ uint32_t cta_rank() {
   return r;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // True on one lane of the (converged) warp. Unlike a lane test, it tells the compiler that one
@@ -317,11 +322,9 @@ __device__ __forceinline__ int seq_cost(int n, int len) {
 }
 static_assert(kTokens == 4 && kBlock == 128, "block_sum's closed form");
 
-// Range g of G nearly equal ones of [0, total), and the range that holds unit t. (total is
-// below 2^30: at most 2^20 + 2^10 tiles of at most 513 + kTileCost units.)
-__device__ __forceinline__ int range_begin(int g, int G, int total) {
-  return g * (total / G) + min(g, total % G);
-}
+// Of G nearly equal ranges of [0, total) -- the first total mod G one longer -- the one that
+// holds unit t. (total is below 2^30: at most 2^20 + 2^10 tiles of at most 513 + kTileCost
+// units.)
 __device__ __forceinline__ int range_of(int t, int G, int total) {
   const int q = total / G, r = total % G, cut = r * (q + 1);
   return t < cut ? t / (q + 1) : r + (t - cut) / q;
@@ -347,29 +350,34 @@ struct Cursor {
   const Plan* P;
   int batch, begin, end, pos, b, tile;
 
+  // Called by whole warps: each search looks at 32 places a step.
   __device__ void init(const Plan& plan, int batch_, int g, int G) {
     P = &plan;
     batch = batch_;
     const int total = plan.cost[batch];
     begin = end = pos = b = tile = 0;
     if (total == 0 || g >= G) return;
-    begin = range_begin(g, G, total);
-    end = range_begin(g + 1, G, total);
-    // the sequence, then the tile, that hold unit `begin`
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (plan.cost[mid] <= begin) lo = mid; else hi = mid - 1;
+    const int q = total / G, r = total - q * G;
+    begin = g * q + min(g, r);
+    end = begin + q + (g < r);
+    // the sequence, then the tile, that hold unit `begin`: the last that starts at or before it
+    b = last_true(batch, [&](int i) { return plan.cost[i] <= begin; });
+    const int n = plan.start[b + 1] - plan.start[b], p = plan.len[b] - n, c = plan.cost[b];
+    tile = last_true((n + kTokens - 1) / kTokens, [&](int i) { return c + tile_offset(p, i) <= begin; });
+    pos = c + tile_offset(p, tile);
+  }
+
+  // The last i of [0, n) with pred(i), which holds from 0 up to some i.
+  template <class F>
+  static __device__ int last_true(int n, F&& pred) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;  // pred(lo) holds
+    for (int step = n > 1024 ? 1024 : n > 32 ? 32 : 1;; step /= 32) {
+      const int i = lo + lane * step;
+      const uint32_t yes = __ballot_sync(0xffffffffu, i < n && pred(i));
+      lo += (31 - __clz(yes)) * step;  // (lane 0 says yes)
+      if (step == 1) return lo;
     }
-    b = lo;
-    const int n = plan.start[b + 1] - plan.start[b], p = plan.len[b] - n;
-    int t0 = 0, t1 = (n + kTokens - 1) / kTokens - 1;
-    while (t0 < t1) {
-      const int mid = (t0 + t1 + 1) >> 1;
-      if (plan.cost[b] + tile_offset(p, mid) <= begin) t0 = mid; else t1 = mid - 1;
-    }
-    tile = t0;
-    pos = plan.cost[b] + tile_offset(p, tile);
   }
 
   __device__ bool next(Item& it) {
@@ -400,6 +408,11 @@ struct Cursor {
 __device__ void build_plan(Smem& S, const ChunkAttnArgs& a, bool report) {
   Plan& P = S.plan;
   uint32_t bits = 0;
+  if (threadIdx.x == kThreads - 1) {
+    // (rows of one table, a fixed distance apart)
+    P.pages = a.kv[0].pages;
+    P.page_stride = a.batch > 1 ? static_cast<int>(a.kv[1].pages - a.kv[0].pages) : 0;
+  }
   for (int b = threadIdx.x; b < a.batch; b += kThreads) {
     const int s0 = a.q_start[b], s1 = a.q_start[b + 1], L = a.seq_lens[b];
     const KvSeq& kv = a.kv[b];
@@ -475,8 +488,8 @@ struct Groups {
     const int g = g0 + lane;
     return g <= last ? pages[g >> shift] : 0;
   }
-  __device__ void init(const KvSeq& s, int g0, int last_, int shift_, int lane) {
-    pages = s.pages;
+  __device__ void init(const int32_t* pages_, int g0, int last_, int shift_, int lane) {
+    pages = pages_;
     last = last_;
     shift = shift_;
     base = g0;
@@ -530,7 +543,8 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
     const int last_group = (it.kend() - 1) / kChunkBoxRows;
     Groups kg, vg;
     if constexpr (kPaged) {
-      kg.init(a.kv[it.b], 2 * it.blk0, last_group, page_shift - 6, lane);
+      kg.init(S.plan.pages + static_cast<long long>(it.b) * S.plan.page_stride, 2 * it.blk0,
+              last_group, page_shift - 6, lane);
       vg = kg;
     }
     // 64 rows from group gr on, `boxes` boxes of 128 bytes a row from column x on
@@ -847,53 +861,56 @@ __device__ __forceinline__ void load8(const void* base, long long at, float (&f)
   }
 }
 
-// FP8: this thread's 128 dimensions of its row of Q, split into e4m3 high and low parts scaled
-// by 2^-e with the row's largest magnitude in [128, 256). Returns e. (bf16 times a power of
-// two is exact in f16 down to 2^-24 of 256; smaller elements round there.) The Q buffer must
-// be free: every S of the previous item has completed.
-__device__ __noinline__ int split_q(Smem& S, const ChunkAttnArgs& a, const Item& it, int rank,
-                                    int row, int half, uint32_t bar_id) {
-  const int tok = it.row0 + kCtaTokens * rank + row / kHeads;
-  const bool real = tok < a.n_rows;  // (a tile's missing tokens take whatever row is there)
-  const uint4* src = reinterpret_cast<const uint4*>(
-      a.q + (static_cast<size_t>(tok) * kHeads + row % kHeads) * kHeadDim + 128 * half);
-  uint4 v[16];
-  float mx = 0.f;
+// FP8: Q of an item, split into e4m3 high and low parts scaled by 2^-e with the row's largest
+// magnitude in [128, 256); e goes to S.q_exp. (bf16 times a power of two is exact in f16 down
+// to 2^-24 of 256; smaller elements round there.) Each softmax warp takes 16 of the CTA's rows,
+// 16 lanes a row and 16 dimensions a lane, so that its loads cover whole lines (one row a
+// thread took 12000 cycles). The Q buffer must be free: every S of the previous item has
+// completed.
+__device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item& it, int rank,
+                                     int swarp, int lane) {
+  constexpr int kRowsWarp = kRows / kSoftmaxWarps;
+  const int part = lane % 16, r0 = swarp * kRowsWarp + lane / 16;
+  const long long row0 = (static_cast<long long>(it.row0) + kCtaTokens * rank) * kHeads;
+  const long long end = static_cast<long long>(a.n_rows) * kHeads;
+  uint4 v[kRowsWarp / 2][2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+  for (int i = 0; i < kRowsWarp / 2; ++i) {
+    // (a tile's missing tokens take whatever rows are there)
+    const long long r = row0 + r0 + 2 * i;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + r * kHeadDim + 16 * part);
+    v[i][0] = r < end ? src[0] : make_uint4(0, 0, 0, 0);
+    v[i][1] = r < end ? src[1] : make_uint4(0, 0, 0, 0);
   }
-  S.xch[half][row] = mx;
-  named_bar_sync(bar_id, 64);
-  mx = fmaxf(mx, S.xch[half ^ 1][row]);
-  named_bar_sync(bar_id, 64);
-  // e >= -100 keeps 2^-e finite; a row with an infinity (its scores are NaN anyhow) takes 0
-  const int e = mx > 0.f && mx <= 3.0e38f ? max(ilogbf(mx) - 7, -100) : 0;
-  const float sc = ldexpf(1.f, -e);
-  uint8_t* hi_row = S.q + half * kQChunkBytes + row * 128;
-  uint8_t* lo_row = hi_row + 2 * kQChunkBytes;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {  // 16 dimensions a piece
+  for (int i = 0; i < kRowsWarp / 2; ++i) {
+    const int r = r0 + 2 * i;
+    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
+                           v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    float mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 128 <= mx 2^-e < 256; e >= -100 keeps 2^-e finite; a row with an infinity (its scores are
+    // NaN anyhow) and one of zeros take 0. (A subnormal mx counts as 2^-127.)
+    const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
+    const int e = mx > 0.f && ex < 255 ? max(ex - 127 - 7, -100) : 0;
+    const float sc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    if (part == 0) S.q_exp[r] = e;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint4 x = v[2 * p + k / 2];
-      const uint32_t w0 = k % 2 ? x.z : x.x, w1 = k % 2 ? x.w : x.y;
       uint32_t h0, l0, h1, l1;
-      split_e4m3x2(pack_f16x2(bf16_lo(w0) * sc, bf16_hi(w0) * sc), h0, l0);
-      split_e4m3x2(pack_f16x2(bf16_lo(w1) * sc, bf16_hi(w1) * sc), h1, l1);
+      split_e4m3x2(pack_f16x2(bf16_lo(w[2 * k]) * sc, bf16_hi(w[2 * k]) * sc), h0, l0);
+      split_e4m3x2(pack_f16x2(bf16_lo(w[2 * k + 1]) * sc, bf16_hi(w[2 * k + 1]) * sc), h1, l1);
       hi[k] = h0 | (h1 << 16);
       lo[k] = l0 | (l1 << 16);
     }
-    *reinterpret_cast<uint4*>(hi_row + ((p ^ (row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(lo_row + ((p ^ (row & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    uint8_t* dst = S.q + (part / 8) * kQChunkBytes + r * 128 + (((part % 8) ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(dst + 2 * kQChunkBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
-  return e;
 }
 
 // A special block's V half in this CTA's ring (its first slot's use `chunk`), by one warp: rows
@@ -1025,17 +1042,25 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
 
   Cursor cur;
   cur.init(S.plan, a.batch, g, G);
-  Item it;
-  while (cur.next(it)) {
+  Item it, nx;
+  bool has = cur.next(it);
+  float mul = mul0;
+  // FP8: the next item's Q into the buffer, once every S of this one is done, and its rows'
+  // factor of the scores
+  auto next_q = [&](const Item& x) {
+    split_q(S, a, x, rank, swarp, lane);
+    fence_proxy_async_smem();
+    named_bar_sync(7, 32 * kSoftmaxWarps);  // q_exp (and every warp's part is in place)
+    const float f = mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[row]) << 23);
+    if (st == 0) remote_arrive_release(q_bar);
+    return f;
+  };
+  if constexpr (kFp8) {
+    if (has) mul = next_q(it);
+  }
+  while (has) {
     const int n = it.blk1 - it.blk0;
-    float mul = mul0;
-    if constexpr (kFp8) {
-      const int e = split_q(S, a, it, rank, row, half, bar);
-      mul = mul0 * ldexpf(1.f, e);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) remote_arrive_release(q_bar);
-    }
+    float next_mul = mul0;
     // keys this row's token sees: positions below lim
     const int lim = it.p0 + min(tok, it.ntok - 1) + 1;
     float m = -INFINITY, base = 0.f, l = 0.f;  // m: raw; base = m mul (0 while m is -inf)
@@ -1159,9 +1184,19 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     chunk += n * (C::kKSlots + C::kVSlots);
 
     // ---- epilogue ----
+    // what the next item needs goes first, while the last product runs
     S.xch[half][row] = l;
+    const bool has_nx = cur.next(nx);
     named_bar_sync(bar, 64);
     l += S.xch[half ^ 1][row];
+    const bool whole = it.whole();
+    if constexpr (kFp8) {
+      if (has_nx) next_mul = next_q(nx);
+    }
+    if (whole) {
+      mbar_wait(&S.stage_free, tiles & 1, abort);
+      ++tiles;
+    }
     mbar_wait(&S.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort);
     tc_fence_after();
     const bool ok = *abort == 0;
@@ -1170,15 +1205,12 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     const uint32_t bad = *static_cast<volatile uint32_t*>(&S.bad[item & 1][half]);
     if (bad != 0) add_late<kFp8>(a, it, bad, tok, head, half, base - C::kPExp, o_addr);
     const bool real = tok < it.ntok;  // (the same for the whole warp)
-    const bool whole = it.whole();
     const int slot = 2 * g + (it.blk0 == 0 ? 1 : 0);
     if (whole) {
       // rounded into the ring, as boxes of [128 rows x 64 dimensions] with 128-byte swizzle,
       // for the helper warp to store (stores of each lane's own row touch 32 lines each: the
       // epilogue took 12000 cycles that way, 3300 after a transposition by shuffles, 1000 so)
       const float inv = v_mul / l;
-      mbar_wait(&S.stage_free, tiles & 1, abort);
-      ++tiles;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t r[2][32];
@@ -1243,8 +1275,10 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
       named_bar_sync(5 + half, 32 * kSoftmaxWarps / 2);
       if (st % 128 == 0) S.bad[item & 1][half] = 0;
     }
-    // (FP8: the next item's Q split writes xch)
-    if constexpr (kFp8) named_bar_sync(bar, 64);
+    // (xch is written again only behind the pair's next barrier)
+    it = nx;
+    has = has_nx;
+    mul = next_mul;
     ++item;
   }
   if (rank == 0 && st == 0) a.info[g] = info;
@@ -1343,7 +1377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&S.kv_empty[i], 1);
       mbar_init(&S.v_full[i], 1);
     }
-    mbar_init(&S.q_full, kFp8 ? 2 * kSoftmaxWarps : 1);
+    mbar_init(&S.q_full, kFp8 ? 2 : 1);
     mbar_init(&S.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
@@ -1361,12 +1395,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&out_map);
   }
   if (warp == 1) pair_tmem_alloc(&S.tmem_base);
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();  // this CTA's barriers are set up
   pdl_launch_dependents();
   pdl_wait();
   build_plan(S, a, blockIdx.x == 0);
   const int G = min(static_cast<int>(gridDim.x) / 2, S.plan.cost[a.batch]);
-  tc_fence_before();
-  cluster_sync();  // both CTAs' barriers are set up (and a CTA-wide barrier)
+  cluster_wait();  // and the other's
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
@@ -1386,7 +1422,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // the last commit of the products reaches both CTAs: neither may be gone by then
   if (warp == 1 && rank != 0) mbar_wait_drain(&S.mma_done, 0);
   __syncwarp();
-  cluster_sync();  // the other CTA's products and arrivals are done with this one's memory
+  cluster_arrive();
+  cluster_wait();  // the other CTA's products and arrivals are done with this one's memory
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
