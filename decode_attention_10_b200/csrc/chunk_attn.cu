@@ -67,7 +67,7 @@ constexpr int kHelperWarp = 2 + kSoftmaxWarps;
 constexpr int kThreads = 32 * (kHelperWarp + 1);
 constexpr int kStageSlots = 4;  // ring slots that a finished tile's 128 x 256 bf16 results take
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
-constexpr int kTileCost = 2;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
+constexpr int kTileCost = 3;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
@@ -521,13 +521,15 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   int item = 0;
   Cursor cur;
   cur.init(S.plan, a.batch, g, G);
-  Item it;
-  while (cur.next(it)) {
+  Item it, nx;
+  bool has = cur.next(it);
+  if (has && leader) {
+    prefetch_tensormap(&maps[it.b].k);
+    prefetch_tensormap(&maps[it.b].v);
+  }
+  while (has) {
     const KvChunkMaps* map = maps + it.b;
-    if (leader) {
-      prefetch_tensormap(&map->k);
-      prefetch_tensormap(&map->v);
-    }
+    const bool has_nx = cur.next(nx);
     if constexpr (!kFp8) {
       if (item > 0) mbar_wait(&S.q_empty, (item - 1) & 1, abort);
       if (leader && !*abort) {
@@ -616,6 +618,14 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
       specials += special;
     };
     load_k(it.blk0);
+    if (has_nx && leader) {
+      // the next item's Q (read once from HBM) on its way to L2, and its tensor maps
+      const int first = nx.row0 + kCtaTokens * static_cast<int>(rank);
+      if (first < a.n_rows)
+        for (int c = 0; c < 4; ++c) tma_prefetch_2d(q_map, 64 * c, first * kHeads);
+      prefetch_tensormap(&maps[nx.b].k);
+      prefetch_tensormap(&maps[nx.b].v);
+    }
     for (int blk = it.blk0; blk < it.blk1; ++blk) {
       if (blk + 1 < it.blk1) load_k(blk + 1);
       load_v(blk);
@@ -628,6 +638,8 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
       }
       if (leader && !*abort) mbar_arrive(&S.stage_free);
     }
+    it = nx;
+    has = has_nx;
     ++item;
   }
   // Before the CTAs may exit, every copy must have landed (after an abort; else all were used):
@@ -920,38 +932,47 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
 template <bool kFp8>
 __device__ __forceinline__ uint32_t clean_v(Smem& S, const Item& it, int blk, uint32_t chunk,
                                             int lane) {
-  constexpr int kPieces = kFp8 ? 8 : 16;  // 16-byte pieces of a key's 128 dimensions
+  constexpr int kBoxes = kFp8 ? 1 : 2;  // boxes of 128 bytes across this CTA's 128 dimensions
   uint8_t* slot0 = S.ring + (chunk % kSlots) * kSlotBytes;
   uint8_t* slot1 = kFp8 ? slot0 + kBoxBytes : S.ring + ((chunk + 1) % kSlots) * kSlotBytes;
-  // keys 64 h .. 64 h + 63 of the block are rows of 128 bytes from here on (bf16: two boxes)
-  auto row_piece = [&](int r, int piece) {
-    uint8_t* half = r < kChunkBoxRows ? slot0 : slot1;
-    return reinterpret_cast<uint4*>(half + (piece / 8) * kBoxBytes + (r % kChunkBoxRows) * 128 +
-                                    (piece % 8) * 16);
-  };
-  const int from = max(0, it.kend() - blk * kBlock);
-  for (int r = from + lane / kPieces; r < kBlock; r += 32 / kPieces)
-    *row_piece(r, lane % kPieces) = make_uint4(0, 0, 0, 0);
+  // late rows: lane = 16-byte piece of the row
   uint32_t bad = 0;
+  uint4 v[kTokens - 1];
+  uint4* at[kTokens - 1];
 #pragma unroll
   for (int i = 0; i < kTokens - 1; ++i) {
     const int r = it.p0 + 1 + i - blk * kBlock;
-    if (i + 1 >= it.ntok || r < 0 || r >= kBlock) continue;
-    bool odd = false;
-    if (lane < kPieces) {
-      const uint4 v = *row_piece(r, lane);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const bool here = i + 1 < it.ntok && r >= 0 && r < kBlock && lane < 8 * kBoxes;
+    at[i] = here ? reinterpret_cast<uint4*>((r < kChunkBoxRows ? slot0 : slot1) + (lane / 8) * kBoxBytes +
+                                            (r % kChunkBoxRows) * 128 + (lane % 8) * 16)
+                 : nullptr;
+    v[i] = here ? *at[i] : make_uint4(0, 0, 0, 0);
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (kFp8)  // a byte of 0x7F or 0xFF
-          odd |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-        else
-          odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
-      }
+  for (int i = 0; i < kTokens - 1; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (kFp8)  // a byte of 0x7F or 0xFF
+        odd |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+      else
+        odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
     }
     if (__any_sync(0xffffffffu, odd)) {
       bad |= 1u << i;
-      if (lane < kPieces) *row_piece(r, lane) = make_uint4(0, 0, 0, 0);
+      if (at[i] != nullptr) *at[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  // the rows from kend on are the rest of each box
+  const int from = max(0, it.kend() - blk * kBlock);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int f = max(0, from - h * kChunkBoxRows);
+    for (int i = f * 8 + lane; i < kChunkBoxRows * 8; i += 32) {
+      uint4* p = reinterpret_cast<uint4*>(h == 0 ? slot0 : slot1) + i;
+      p[0] = make_uint4(0, 0, 0, 0);
+      if constexpr (kBoxes == 2) p[kBoxBytes / 16] = make_uint4(0, 0, 0, 0);
     }
   }
   return bad;

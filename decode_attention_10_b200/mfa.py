@@ -141,6 +141,11 @@ def _stream(stream: Optional[torch.cuda.Stream] = None) -> int:
     return s.cuda_stream
 
 
+def _raw_stream(dev: int) -> int:
+    """The handle of the current stream of device `dev`, without a Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return KV_BF16
@@ -188,6 +193,7 @@ class KVCache:
                "mfa_kv_table_init")
         self.desc = KvCacheDesc(self.batch, self.dtype, self.k_scale, self.v_scale,
                                 self.table.data_ptr(), 0)
+        self.ref = ctypes.byref(self.desc)
 
 
 class PagedKVCache:
@@ -233,6 +239,7 @@ class PagedKVCache:
                "mfa_kv_table_init_paged")
         self.desc = KvCacheDesc(self.batch, self.dtype, self.k_scale, self.v_scale,
                                 self.table.data_ptr(), self.page_size)
+        self.ref = ctypes.byref(self.desc)
 
 
 class BlockFP8Weight:
@@ -265,7 +272,8 @@ class Workspace:
             raise ValueError(f"batch {batch} out of range (or no CUDA device)")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8,
                                device=device if device is not None else "cuda")
-        _check(lib.mfa_workspace_init(self.buf.data_ptr(), self.nbytes, _stream(stream)),
+        self.addr = self.buf.data_ptr()
+        _check(lib.mfa_workspace_init(self.addr, self.nbytes, _stream(stream)),
                "mfa_workspace_init")
 
     @property
@@ -309,6 +317,7 @@ class Rope:
         self.n_axes = max(axes) + 1
         self.desc = RopeDesc(_ptr(table), int(table.shape[0]), self.rot_dim, int(interleaved),
                              self.n_axes, (ctypes.c_uint8 * (HEAD_DIM // 2))(*axes))
+        self.ref = ctypes.byref(self.desc)
 
 
 def get_error(ws: Workspace, stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -369,26 +378,29 @@ def decode_layer(x, w_qdown, gamma, w_qup, w_k, w_v, cache: KVCache, seq_lens,
     return q_out, out
 
 
-def _token_batch(cache, q_start: torch.Tensor, seq_lens: torch.Tensor):
-    """Checks of a ragged batch's two arrays."""
-    for t, n, what in ((q_start, cache.batch + 1, "q_start"), (seq_lens, cache.batch, "seq_lens")):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
-            raise ValueError(f"{what} must be int32 [{n}]")
+# The two calls below are made per layer and step, and a serving loop's host thread pays for
+# every attribute it reads of a tensor: each argument is checked by one expression of the few
+# that say all of it, and _refuse finds the words when one does not hold.
+_BF16, _I32 = torch.bfloat16, torch.int32
+_Q_TAIL = (N_HEADS, HEAD_DIM)
 
 
-def _rows(t: torch.Tensor, n_rows: int, what: str):
-    """A [n_rows, 256] bf16 CUDA tensor whose rows may lie apart: its pointer and row stride."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n_rows, HEAD_DIM) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA bf16 [{n_rows}, {HEAD_DIM}]")
-    if t.stride(1) != 1:
-        raise ValueError(f"the rows of {what} must be dense")
-    return t.data_ptr(), t.stride(0) if n_rows > 1 else max(HEAD_DIM, t.stride(0) // 8 * 8)
-
-
-def _queries(t: torch.Tensor, n_rows: int, what: str) -> int:
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n_rows, N_HEADS, HEAD_DIM):
-        raise ValueError(f"{what} must be bf16 [{n_rows}, {N_HEADS}, {HEAD_DIM}]")
-    return _ptr(t)
+def _refuse(dev: int, **tensors):
+    """Raise for the first of the tensors name=(tensor, dtype, shape, dense) that is not so."""
+    for what, (t, dtype, shape, dense) in tensors.items():
+        if t.dtype is not dtype or tuple(t.shape) != shape:
+            name = str(dtype).replace("torch.", "")
+            raise ValueError(f"{what} must be {name} {list(shape)}, not "
+                             f"{str(t.dtype).replace('torch.', '')} {list(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"expected a CUDA tensor for {what}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"expected a contiguous tensor for {what}")
+        if not dense and t.stride(-1) != 1:
+            raise ValueError(f"the rows of {what} must be dense")
+    raise ValueError("unsupported arguments")
 
 
 def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
@@ -399,30 +411,49 @@ def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
     (q_out; q itself may be given). Rows q_start[b] .. q_start[b + 1] are sequence b's, the
     last of its seq_lens[b] positions; k and v may be views with spaced rows. positions: int32
     [axes, T] or [T]; None: a token's cache row."""
-    lib = load()
-    n = int(k.shape[0])
-    _token_batch(cache, q_start, seq_lens)
-    kp, k_ld = _rows(k, n, "k")
-    vp, v_ld = _rows(v, n, "v")
-    qp = qop = None
+    lib = _lib or load()
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    n, batch = k.shape[0], cache.batch
+    row, k_step, v_step = (n, HEAD_DIM), k.stride(), v.stride()
+    if (k.dtype is not _BF16 or v.dtype is not _BF16 or k.shape != row or v.shape != row
+            or k.get_device() != dev or v.get_device() != dev or k_step[1] != 1 or v_step[1] != 1
+            or q_start.dtype is not _I32 or q_start.numel() != batch + 1
+            or seq_lens.dtype is not _I32 or seq_lens.numel() != batch
+            or q_start.get_device() != dev or seq_lens.get_device() != dev
+            or not q_start.is_contiguous() or not seq_lens.is_contiguous()):
+        _refuse(dev, k=(k, _BF16, row, False), v=(v, _BF16, row, False),
+                q_start=(q_start, _I32, (batch + 1,), True),
+                seq_lens=(seq_lens, _I32, (batch,), True))
+    qp = qop = pp = rp = None
     if q is not None:
-        qp = _queries(q, n, "q")
         if q_out is None:
             q_out = torch.empty_like(q)
-        qop = _queries(q_out, n, "q_out")
+        shape = (n, *_Q_TAIL)
+        if (q.dtype is not _BF16 or q_out.dtype is not _BF16 or q.shape != shape
+                or q_out.shape != shape or q.get_device() != dev or q_out.get_device() != dev
+                or not q.is_contiguous() or not q_out.is_contiguous()):
+            _refuse(dev, q=(q, _BF16, shape, True), q_out=(q_out, _BF16, shape, True))
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
+    if rope is not None:
+        rp = rope.ref
     if positions is not None:
         axes = rope.n_axes if rope is not None else 0
-        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) \
-                or positions.numel() != axes * n or positions.shape[-1] != n:
-            raise ValueError(f"positions must be int32 [{axes}, {n}]")
-    ws = ws if ws is not None else Workspace(cache.batch, k.device)
-    _check(lib.mfa_rope_append(qp, kp, k_ld, vp, v_ld,
-                               ctypes.byref(rope.desc) if rope is not None else None,
-                               _ptr(positions), ctypes.byref(cache.desc), _ptr(q_start),
-                               _ptr(seq_lens), n, qop, ws.ptr, ws.nbytes, _stream(stream)),
-           "mfa_rope_append")
+        shape = (axes, n) if axes != 1 or positions.dim() == 2 else (n,)
+        if (positions.dtype is not _I32 or positions.shape != shape
+                or positions.get_device() != dev or not positions.is_contiguous()):
+            _refuse(dev, positions=(positions, _I32, shape, True))
+        pp = positions.data_ptr()
+    if ws is None:
+        ws = Workspace(batch, k.device)
+    # (the row stride of a single row says nothing)
+    st = lib.mfa_rope_append(qp, k.data_ptr(), k_step[0] if n > 1 else HEAD_DIM, v.data_ptr(),
+                             v_step[0] if n > 1 else HEAD_DIM, rp, pp, cache.ref,
+                             q_start.data_ptr(), seq_lens.data_ptr(), n, qop, ws.addr, ws.nbytes,
+                             _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise MfaError(st, "mfa_rope_append")
     return q_out
 
 
@@ -431,15 +462,29 @@ def chunk_attn(q, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
     """mfa_chunk_attn: causal attention of a ragged batch of new tokens q [T, 64, 256] over the
     cache (which holds their keys and values already); rows as in rope_append. Rows of no
     sequence are left as they were in `out`. ws: a ChunkWorkspace."""
-    lib = load()
-    n = int(q.shape[0])
-    _token_batch(cache, q_start, seq_lens)
+    lib = _lib or load()
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    n, batch = q.shape[0], cache.batch
     if out is None:
         out = torch.empty_like(q)
-    ws = ws if ws is not None else ChunkWorkspace(cache.batch, q.device)
-    _check(lib.mfa_chunk_attn(_queries(q, n, "q"), ctypes.byref(cache.desc), _ptr(q_start),
-                              _ptr(seq_lens), n, float(scale), _queries(out, n, "out"), ws.ptr,
-                              ws.nbytes, _stream(stream)), "mfa_chunk_attn")
+    shape = (n, *_Q_TAIL)
+    if (q.dtype is not _BF16 or out.dtype is not _BF16 or q.shape != shape or out.shape != shape
+            or q.get_device() != dev or out.get_device() != dev or not q.is_contiguous()
+            or not out.is_contiguous()
+            or q_start.dtype is not _I32 or q_start.numel() != batch + 1
+            or seq_lens.dtype is not _I32 or seq_lens.numel() != batch
+            or q_start.get_device() != dev or seq_lens.get_device() != dev
+            or not q_start.is_contiguous() or not seq_lens.is_contiguous()):
+        _refuse(dev, q_start=(q_start, _I32, (batch + 1,), True),
+                seq_lens=(seq_lens, _I32, (batch,), True), q=(q, _BF16, shape, True),
+                out=(out, _BF16, shape, True))
+    if ws is None:
+        ws = ChunkWorkspace(batch, q.device)
+    st = lib.mfa_chunk_attn(q.data_ptr(), cache.ref, q_start.data_ptr(), seq_lens.data_ptr(), n,
+                            scale, out.data_ptr(), ws.addr, ws.nbytes,
+                            _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise MfaError(st, "mfa_chunk_attn")
     return out
 
 

@@ -82,17 +82,19 @@ def test_binding_refusals():
     starts, lens = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     q = torch.zeros(4, 64, 256, dtype=torch.bfloat16)
     kv = torch.zeros(4, 512, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="q_start"):
+    with pytest.raises(ValueError, match="q_start must be"):
         mfa.chunk_attn(q, cache, starts[:2], lens, ws=mfa)
-    with pytest.raises(ValueError, match="seq_lens"):
+    with pytest.raises(ValueError, match="CUDA tensor for q_start"):
         mfa.chunk_attn(q, cache, starts, lens.long(), ws=mfa)
     for bad in (q.float(), q[:, :32], q.view(4, 256, 64)):
-        with pytest.raises(ValueError, match="q must be"):
+        with pytest.raises(ValueError, match="must be"):
             mfa.chunk_attn(bad, cache, starts, lens, out=q, ws=mfa)
     with pytest.raises(ValueError, match="CUDA"):
         mfa.chunk_attn(q, cache, starts, lens, out=q, ws=mfa)
-    with pytest.raises(ValueError, match="k must be"):
+    with pytest.raises(ValueError, match="CUDA tensor for k"):
         mfa.rope_append(q, kv[:, :256], kv[:, 256:], cache, starts, lens, ws=mfa)
+    with pytest.raises(ValueError, match="v must be"):
+        mfa.rope_append(q, kv[:, :256], kv[:, 250:], cache, starts, lens, ws=mfa)
     with pytest.raises(ValueError, match="rot_dim"):
         mfa.Rope(torch.zeros(5, 24))
     with pytest.raises(ValueError, match="float32"):
