@@ -7,12 +7,18 @@
 // kernel only multiplies (float32, one rounding at the end).
 //
 // One block per token. A row of 256 dimensions is 16 units of 16 dimensions -- a unit is
-// eight whole pairs, so a thread rotates what it has loaded -- and the 64 query heads are 16
-// groups of 4: thread (group, unit) takes its unit of four heads, eight 16-byte loads in
-// flight before anything is waited for. The two half-warps of groups 0 and 1 take the K and
-// the V row as well. Everything a token needs to know (its sequence, cache row, page and
-// angles) is looked up while its 32 KB of queries arrive; the angles are shared by the block
-// through shared memory, since all 65 rows turn by the same ones.
+// eight whole pairs, so a thread rotates what it has loaded. Thread (group, unit) takes its
+// unit of 64 / groups heads, all its 16-byte loads in flight before anything is waited for.
+// Groups 0 and 1 take the K and the V row as well. Everything a token needs to know (its
+// sequence, cache row, page and angles) is looked up while its 32 KB of queries arrive; the
+// angles are shared by the block through shared memory, since all 65 rows turn by the same
+// ones.
+//
+// Bound by HBM: 32 KB in and out a token. Blocks of 128 threads (8 heads and sixteen 16-byte
+// loads a thread, 4 blocks an SM) move 6.5 TB/s, all of a copy's rate: 8409 tokens, bf16 cache,
+// 88.8 us; 256 threads (4 heads) 113 us, 512 (2 heads) 168 us, since a block's chain of
+// look-ups is then paid for fewer bytes a thread. Where the tokens fill no more than the SMs,
+// that chain is all there is, and more threads a block shorten it (kSmallRows).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -22,11 +28,11 @@
 namespace mfa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnits = kHeadDim / 16;              // 16-dimension units of a row
-constexpr int kGroups = kThreads / kUnits;         // groups of heads
-constexpr int kGroupHeads = kHeads / kGroups;      // heads of a thread
+constexpr int kUnits = kHeadDim / 16;  // 16-dimension units of a row
 constexpr int kMaxPairs = kHeadDim / 2;
+// Up to one token an SM, blocks of 512 threads; above it blocks of 128. Measured at 64, 148,
+// 200 and 444 tokens: 3.3, 3.3, 5.7, 10.1 us with 512 threads, 3.9, 5.0, 5.2, 6.8 with 128.
+constexpr int kSmallRows = 148;
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -88,8 +94,12 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
   return make_uint2(w[0], w[1]);
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
+  constexpr int kGroups = kThreads / kUnits;     // groups of heads
+  constexpr int kGroupHeads = kHeads / kGroups;  // heads of a thread
+  static_assert(kGroups >= 2 && kThreads >= kMaxPairs, "K, V and the angles each in one go");
   __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
   const int row = blockIdx.x, tid = threadIdx.x;
   const int u = tid % kUnits, group = tid / kUnits;
@@ -190,7 +200,9 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s) {
-  return launch_pdl(rope_append_kernel, dim3(a.n_rows), dim3(kThreads), 0, s, a);
+  if (a.n_rows <= kSmallRows)
+    return launch_pdl(rope_append_kernel<512>, dim3(a.n_rows), dim3(512), 0, s, a);
+  return launch_pdl(rope_append_kernel<128>, dim3(a.n_rows), dim3(128), 0, s, a);
 }
 
 }  // namespace mfa

@@ -86,15 +86,17 @@ def test_binding_refusals():
         mfa.chunk_attn(q, cache, starts[:2], lens, ws=mfa)
     with pytest.raises(ValueError, match="CUDA tensor for q_start"):
         mfa.chunk_attn(q, cache, starts, lens.long(), ws=mfa)
-    for bad in (q.float(), q[:, :32], q.view(4, 256, 64)):
-        with pytest.raises(ValueError, match="must be"):
-            mfa.chunk_attn(bad, cache, starts, lens, out=q, ws=mfa)
     with pytest.raises(ValueError, match="CUDA"):
         mfa.chunk_attn(q, cache, starts, lens, out=q, ws=mfa)
+    with pytest.raises(ValueError, match="seq_lens must be"):
+        mfa._refuse(0, seq_lens=(lens.long(), torch.int32, (2,), True))
+    for bad in (q.float(), q[:, :32], q.view(4, 256, 64)):
+        with pytest.raises(ValueError, match="q must be"):
+            mfa._refuse(0, q=(bad, torch.bfloat16, (4, 64, 256), True))
     with pytest.raises(ValueError, match="CUDA tensor for k"):
         mfa.rope_append(q, kv[:, :256], kv[:, 256:], cache, starts, lens, ws=mfa)
     with pytest.raises(ValueError, match="v must be"):
-        mfa.rope_append(q, kv[:, :256], kv[:, 250:], cache, starts, lens, ws=mfa)
+        mfa._refuse(0, v=(kv[:, 250:], torch.bfloat16, (4, 256), False))
     with pytest.raises(ValueError, match="rot_dim"):
         mfa.Rope(torch.zeros(5, 24))
     with pytest.raises(ValueError, match="float32"):
