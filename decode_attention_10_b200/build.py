@@ -1,19 +1,22 @@
-"""Build libmfa.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libmfa.so (the C-ABI library) in-tree with nvcc for sm_100a, and mfa_torch.so (the
+binding of its chunk calls for torch tensors) with the host compiler.
 
     python -m decode_attention_10_b200.build [--verbose]
 
-The library is written next to this file so that it travels with the source tree.
+Both are written next to this file so that they travel with the source tree.
 """
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmfa.so")
+BINDING = os.path.join(HERE, "mfa_torch.so")
 SOURCES = ["abi.cu", "query_path.cu", "gemm_tc.cu", "attention_tc.cu", "out_proj.cu", "noalloc.cu",
            "selftest.cu", "split_plan.cu", "rope_append.cu", "chunk_attn.cu"]
 HEADERS = ["mfa_internal.cuh", "attn_plan.cuh", "sm100.cuh"]
@@ -42,7 +45,38 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(ROOT, "include", "mfa.h"), os.path.abspath(__file__)]
+    if (not force and os.path.exists(BINDING)
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)):
+        return BINDING
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
+           sysconfig.get_paths()["include"]]
+    libs = os.path.join(base, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in inc], src, "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = build_library(force, verbose)
+    build_binding(force, verbose)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     nvcc = nvcc_path()

@@ -6,6 +6,7 @@ There is no fallback: if the library is missing, the first call raises.
 """
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -13,6 +14,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmfa.so")
+BINDING_PATH = os.path.join(_HERE, "mfa_torch.so")
 
 HIDDEN, Q_RANK, N_HEADS, HEAD_DIM = 7168, 2048, 64, 256
 MAX_CONTEXT, MAX_BATCH = 65536, 1024
@@ -102,22 +104,29 @@ class MfaError(RuntimeError):
 
 
 _lib = None
+_chunk = None  # mfa_torch: the chunk calls for torch tensors (csrc/binding.cpp)
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libmfa.so (once). Raises if it has not been built."""
-    global _lib
+    """Load libmfa.so and mfa_torch.so (once). Raises if they have not been built."""
+    global _lib, _chunk
     if _lib is not None:
         return _lib
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with "
-                           "`python -m decode_attention_10_b200.build`")
+    for p in (path, BINDING_PATH):
+        if not os.path.exists(p):
+            raise RuntimeError(f"{p} is missing: build it with "
+                               "`python -m decode_attention_10_b200.build`")
     lib = ctypes.CDLL(path)
     for name, (res, args) in _SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _lib = lib
+    spec = importlib.util.spec_from_file_location("mfa_torch", BINDING_PATH)
+    chunk = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(chunk)
+    chunk.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (lib.mfa_rope_append, lib.mfa_chunk_attn)))
+    _lib, _chunk = lib, chunk
     return lib
 
 
@@ -139,11 +148,6 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _stream(stream: Optional[torch.cuda.Stream] = None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
-
-
-def _raw_stream(dev: int) -> int:
-    """The handle of the current stream of device `dev`, without a Stream object around it."""
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -193,7 +197,7 @@ class KVCache:
                "mfa_kv_table_init")
         self.desc = KvCacheDesc(self.batch, self.dtype, self.k_scale, self.v_scale,
                                 self.table.data_ptr(), 0)
-        self.ref = ctypes.byref(self.desc)
+        self.addr = ctypes.addressof(self.desc)
 
 
 class PagedKVCache:
@@ -239,7 +243,7 @@ class PagedKVCache:
                "mfa_kv_table_init_paged")
         self.desc = KvCacheDesc(self.batch, self.dtype, self.k_scale, self.v_scale,
                                 self.table.data_ptr(), self.page_size)
-        self.ref = ctypes.byref(self.desc)
+        self.addr = ctypes.addressof(self.desc)
 
 
 class BlockFP8Weight:
@@ -317,7 +321,7 @@ class Rope:
         self.n_axes = max(axes) + 1
         self.desc = RopeDesc(_ptr(table), int(table.shape[0]), self.rot_dim, int(interleaved),
                              self.n_axes, (ctypes.c_uint8 * (HEAD_DIM // 2))(*axes))
-        self.ref = ctypes.byref(self.desc)
+        self.addr = ctypes.addressof(self.desc)
 
 
 def get_error(ws: Workspace, stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -378,29 +382,25 @@ def decode_layer(x, w_qdown, gamma, w_qup, w_k, w_v, cache: KVCache, seq_lens,
     return q_out, out
 
 
-# The two calls below are made per layer and step, and a serving loop's host thread pays for
-# every attribute it reads of a tensor: each argument is checked by one expression of the few
-# that say all of it, and _refuse finds the words when one does not hold.
-_BF16, _I32 = torch.bfloat16, torch.int32
-_Q_TAIL = (N_HEADS, HEAD_DIM)
-
-
-def _refuse(dev: int, **tensors):
-    """Raise for the first of the tensors name=(tensor, dtype, shape, dense) that is not so."""
-    for what, (t, dtype, shape, dense) in tensors.items():
-        if t.dtype is not dtype or tuple(t.shape) != shape:
-            name = str(dtype).replace("torch.", "")
-            raise ValueError(f"{what} must be {name} {list(shape)}, not "
-                             f"{str(t.dtype).replace('torch.', '')} {list(t.shape)}")
-        if not t.is_cuda:
-            raise ValueError(f"expected a CUDA tensor for {what}")
-        if t.get_device() != dev:
-            raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-        if dense and not t.is_contiguous():
-            raise ValueError(f"expected a contiguous tensor for {what}")
-        if not dense and t.stride(-1) != 1:
-            raise ValueError(f"the rows of {what} must be dense")
-    raise ValueError("unsupported arguments")
+def _refuse(status: int, where: str, *tensors):
+    """Raise for what a call of mfa_torch returned: the library's status, or -1 - i for the
+    i-th of the tensors (name, tensor, dtype, shape, dense)."""
+    if status > 0:
+        raise MfaError(status, where)
+    what, t, dtype, shape, dense = tensors[-1 - status]
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a tensor")
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {str(dtype).replace('torch.', '')} {list(shape)}, not "
+                         f"{str(t.dtype).replace('torch.', '')} {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if dense:
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    raise ValueError(f"{what}: its rows must be dense and less than 2^31 elements apart")
 
 
 def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
@@ -411,49 +411,30 @@ def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
     (q_out; q itself may be given). Rows q_start[b] .. q_start[b + 1] are sequence b's, the
     last of its seq_lens[b] positions; k and v may be views with spaced rows. positions: int32
     [axes, T] or [T]; None: a token's cache row."""
-    lib = _lib or load()
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
-    n, batch = k.shape[0], cache.batch
-    row, k_step, v_step = (n, HEAD_DIM), k.stride(), v.stride()
-    if (k.dtype is not _BF16 or v.dtype is not _BF16 or k.shape != row or v.shape != row
-            or k.get_device() != dev or v.get_device() != dev or k_step[1] != 1 or v_step[1] != 1
-            or q_start.dtype is not _I32 or q_start.numel() != batch + 1
-            or seq_lens.dtype is not _I32 or seq_lens.numel() != batch
-            or q_start.get_device() != dev or seq_lens.get_device() != dev
-            or not q_start.is_contiguous() or not seq_lens.is_contiguous()):
-        _refuse(dev, k=(k, _BF16, row, False), v=(v, _BF16, row, False),
-                q_start=(q_start, _I32, (batch + 1,), True),
-                seq_lens=(seq_lens, _I32, (batch,), True))
-    qp = qop = pp = rp = None
-    if q is not None:
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        shape = (n, *_Q_TAIL)
-        if (q.dtype is not _BF16 or q_out.dtype is not _BF16 or q.shape != shape
-                or q_out.shape != shape or q.get_device() != dev or q_out.get_device() != dev
-                or not q.is_contiguous() or not q_out.is_contiguous()):
-            _refuse(dev, q=(q, _BF16, shape, True), q_out=(q_out, _BF16, shape, True))
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if rope is not None:
-        rp = rope.ref
-    if positions is not None:
-        axes = rope.n_axes if rope is not None else 0
-        shape = (axes, n) if axes != 1 or positions.dim() == 2 else (n,)
-        if (positions.dtype is not _I32 or positions.shape != shape
-                or positions.get_device() != dev or not positions.is_contiguous()):
-            _refuse(dev, positions=(positions, _I32, shape, True))
-        pp = positions.data_ptr()
+    if _lib is None:
+        load()
+    batch = cache.batch
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    elif q_out is None:
+        q_out = torch.empty_like(q)
     if ws is None:
         ws = Workspace(batch, k.device)
-    # (the row stride of a single row says nothing)
-    st = lib.mfa_rope_append(qp, k.data_ptr(), k_step[0] if n > 1 else HEAD_DIM, v.data_ptr(),
-                             v_step[0] if n > 1 else HEAD_DIM, rp, pp, cache.ref,
-                             q_start.data_ptr(), seq_lens.data_ptr(), n, qop, ws.addr, ws.nbytes,
-                             _raw_stream(dev) if stream is None else stream.cuda_stream)
+    addr, axes = (0, 0) if rope is None else (rope.addr, rope.n_axes)
+    st = _chunk.rope_append(q, k, v, cache.addr, batch, q_start, seq_lens, addr, axes, positions,
+                            q_out, ws.addr, ws.nbytes,
+                            None if stream is None else stream.cuda_stream)
     if st != 0:
-        raise MfaError(st, "mfa_rope_append")
+        n = k.shape[0]
+        row, heads = (n, HEAD_DIM), (n, N_HEADS, HEAD_DIM)
+        _refuse(st, "mfa_rope_append", ("k", k, torch.bfloat16, row, False),
+                ("v", v, torch.bfloat16, row, False),
+                ("q_start", q_start, torch.int32, (batch + 1,), True),
+                ("seq_lens", seq_lens, torch.int32, (batch,), True),
+                ("q", q, torch.bfloat16, heads, True),
+                ("q_out", q_out, torch.bfloat16, heads, True),
+                ("positions", positions, torch.int32, (axes, n), True))
     return q_out
 
 
@@ -462,29 +443,21 @@ def chunk_attn(q, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
     """mfa_chunk_attn: causal attention of a ragged batch of new tokens q [T, 64, 256] over the
     cache (which holds their keys and values already); rows as in rope_append. Rows of no
     sequence are left as they were in `out`. ws: a ChunkWorkspace."""
-    lib = _lib or load()
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
-    n, batch = q.shape[0], cache.batch
+    if _lib is None:
+        load()
+    batch = cache.batch
     if out is None:
         out = torch.empty_like(q)
-    shape = (n, *_Q_TAIL)
-    if (q.dtype is not _BF16 or out.dtype is not _BF16 or q.shape != shape or out.shape != shape
-            or q.get_device() != dev or out.get_device() != dev or not q.is_contiguous()
-            or not out.is_contiguous()
-            or q_start.dtype is not _I32 or q_start.numel() != batch + 1
-            or seq_lens.dtype is not _I32 or seq_lens.numel() != batch
-            or q_start.get_device() != dev or seq_lens.get_device() != dev
-            or not q_start.is_contiguous() or not seq_lens.is_contiguous()):
-        _refuse(dev, q_start=(q_start, _I32, (batch + 1,), True),
-                seq_lens=(seq_lens, _I32, (batch,), True), q=(q, _BF16, shape, True),
-                out=(out, _BF16, shape, True))
     if ws is None:
         ws = ChunkWorkspace(batch, q.device)
-    st = lib.mfa_chunk_attn(q.data_ptr(), cache.ref, q_start.data_ptr(), seq_lens.data_ptr(), n,
-                            scale, out.data_ptr(), ws.addr, ws.nbytes,
-                            _raw_stream(dev) if stream is None else stream.cuda_stream)
+    st = _chunk.chunk_attn(q, cache.addr, batch, q_start, seq_lens, scale, out, ws.addr,
+                           ws.nbytes, None if stream is None else stream.cuda_stream)
     if st != 0:
-        raise MfaError(st, "mfa_chunk_attn")
+        heads = (q.shape[0], N_HEADS, HEAD_DIM)
+        _refuse(st, "mfa_chunk_attn", ("q", q, torch.bfloat16, heads, True),
+                ("q_start", q_start, torch.int32, (batch + 1,), True),
+                ("seq_lens", seq_lens, torch.int32, (batch,), True),
+                ("out", out, torch.bfloat16, heads, True))
     return out
 
 

@@ -77,26 +77,41 @@ def test_rope_append_refusals(lib):
     assert call(c=kv(dtype=9)) == 2
 
 
-def test_binding_refusals():
-    cache = type("C", (), {"batch": 2})()
+def test_binding_refusals(lib):
+    # (a workspace and a cache that no call gets as far as using)
+    ws = type("W", (), {"addr": 4096, "nbytes": BIG})()
+    desc = mfa.KvCacheDesc(2, 0, 1.0, 1.0, 4096, 0)
+    cache = type("C", (), {"batch": 2, "addr": ctypes.addressof(desc)})()
     starts, lens = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     q = torch.zeros(4, 64, 256, dtype=torch.bfloat16)
     kv = torch.zeros(4, 512, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="q_start must be"):
-        mfa.chunk_attn(q, cache, starts[:2], lens, ws=mfa)
-    with pytest.raises(ValueError, match="CUDA tensor for q_start"):
-        mfa.chunk_attn(q, cache, starts, lens.long(), ws=mfa)
-    with pytest.raises(ValueError, match="CUDA"):
-        mfa.chunk_attn(q, cache, starts, lens, out=q, ws=mfa)
-    with pytest.raises(ValueError, match="seq_lens must be"):
-        mfa._refuse(0, seq_lens=(lens.long(), torch.int32, (2,), True))
-    for bad in (q.float(), q[:, :32], q.view(4, 256, 64)):
+    k, v = kv[:, :256], kv[:, 256:]
+    with pytest.raises(ValueError, match="q: expected a CUDA tensor"):
+        mfa.chunk_attn(q, cache, starts, lens, out=q, ws=ws)
+    with pytest.raises(ValueError, match="k: expected a CUDA tensor"):
+        mfa.rope_append(q, k, v, cache, starts, lens, ws=ws)
+    with pytest.raises(ValueError, match="q_out without q"):
+        mfa.rope_append(None, k, v, cache, starts, lens, q_out=q, ws=ws)
+    with pytest.raises(TypeError, match="k must be a tensor"):
+        mfa.rope_append(None, type("K", (), {"shape": (4,)})(),
+                        v, cache, starts, lens, ws=ws)
+    for bad in (q.float(), q[:, :32], q.view(4, 256, 64), q[0]):
         with pytest.raises(ValueError, match="q must be"):
-            mfa._refuse(0, q=(bad, torch.bfloat16, (4, 64, 256), True))
-    with pytest.raises(ValueError, match="CUDA tensor for k"):
-        mfa.rope_append(q, kv[:, :256], kv[:, 256:], cache, starts, lens, ws=mfa)
-    with pytest.raises(ValueError, match="v must be"):
-        mfa._refuse(0, v=(kv[:, 250:], torch.bfloat16, (4, 256), False))
+            mfa.chunk_attn(bad, cache, starts, lens, out=q, ws=ws)
+    for bad in (k.float(), kv[:, :255], kv):
+        with pytest.raises(ValueError, match="k must be"):
+            mfa.rope_append(None, bad, v, cache, starts, lens, ws=ws)
+    # the words for each of the other arguments
+    for args, words in ((("v", kv[:, 250:], torch.bfloat16, (4, 256), False), "v must be bfloat16"),
+                        (("seq_lens", lens.long(), torch.int32, (2,), True), "seq_lens must be int32"),
+                        (("q_start", starts[:2], torch.int32, (3,), True), "q_start must be int32")):
+        with pytest.raises(ValueError, match=words):
+            mfa._refuse(-1, "", args)
+    with pytest.raises(mfa.MfaError, match="MFA_ERR_WORKSPACE"):
+        mfa._refuse(4, "x")
+    for name, n in (("rope_append", 14), ("chunk_attn", 10), ("bind", 2)):
+        with pytest.raises(TypeError):
+            getattr(mfa._chunk, name)(*[0] * (n - 1))
     with pytest.raises(ValueError, match="rot_dim"):
         mfa.Rope(torch.zeros(5, 24))
     with pytest.raises(ValueError, match="float32"):
