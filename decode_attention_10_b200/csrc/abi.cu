@@ -655,7 +655,7 @@ mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* 
   if (resident <= 0) return MFA_ERR_CUDA;
   a.pairs = resident < slots ? resident : slots;
   CUtensorMap q_map, out_map;
-  if (!encode_2d(&q_map, q, (uint64_t)n_rows * kHeads, kHeadDim, 2, 64, 128) ||
+  if (!encode_2d(&q_map, q, (uint64_t)n_rows * kHeads, kHeadDim, 2, 64, 64) ||
       !encode_2d(&out_map, out, (uint64_t)n_rows * kHeads, kHeadDim, 2, 64, 64))
     return MFA_ERR_CUDA;
   return cuda_status(launch_chunk_attn(q_map, out_map, a, static_cast<cudaStream_t>(stream)));

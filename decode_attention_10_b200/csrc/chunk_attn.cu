@@ -534,9 +534,13 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
       if (item > 0) mbar_wait(&S.q_empty, (item - 1) & 1, abort);
       if (leader && !*abort) {
         if (rank == 0) mbar_arrive_expect_tx(&S.q_full, 2 * 4 * kQChunkBytes);
-        const int y = (it.row0 + kCtaTokens * rank) * kHeads;
-        for (int c = 0; c < 4; ++c)
-          pair_load_2d(S.q + c * kQChunkBytes, q_map, 64 * c, y, q_bar, once);
+        for (int k = 0; k < kCtaTokens; ++k) {
+          // tokens that the tile lacks: rows past the end of q, which read as zeros
+          const int tok = kCtaTokens * static_cast<int>(rank) + k;
+          const int y = (tok < it.ntok ? it.row0 + tok : a.n_rows) * kHeads;
+          for (int c = 0; c < 4; ++c)
+            pair_load_2d(S.q + c * kQChunkBytes + k * kHeads * 128, q_map, 64 * c, y, q_bar, once);
+        }
       }
     }
     // one tile of the sequence reads its rows once; several find them in L2
@@ -620,9 +624,8 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
     load_k(it.blk0);
     if (has_nx && leader) {
       // the next item's Q (read once from HBM) on its way to L2, and its tensor maps
-      const int first = nx.row0 + kCtaTokens * static_cast<int>(rank);
-      if (first < a.n_rows)
-        for (int c = 0; c < 4; ++c) tma_prefetch_2d(q_map, 64 * c, first * kHeads);
+      for (int tok = kCtaTokens * rank; tok < min(kCtaTokens * static_cast<int>(rank + 1), nx.ntok); ++tok)
+        for (int c = 0; c < 4; ++c) tma_prefetch_2d(q_map, 64 * c, (nx.row0 + tok) * kHeads);
       prefetch_tensormap(&maps[nx.b].k);
       prefetch_tensormap(&maps[nx.b].v);
     }
@@ -884,15 +887,14 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
   constexpr int kRowsWarp = kRows / kSoftmaxWarps;
   const int part = lane % 16, r0 = swarp * kRowsWarp + lane / 16;
   const long long row0 = (static_cast<long long>(it.row0) + kCtaTokens * rank) * kHeads;
-  const long long end = static_cast<long long>(a.n_rows) * kHeads;
+  const int rows = (it.ntok - kCtaTokens * rank) * kHeads;  // (those of missing tokens are zero)
   uint4 v[kRowsWarp / 2][2];
 #pragma unroll
   for (int i = 0; i < kRowsWarp / 2; ++i) {
-    // (a tile's missing tokens take whatever rows are there)
-    const long long r = row0 + r0 + 2 * i;
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + r * kHeadDim + 16 * part);
-    v[i][0] = r < end ? src[0] : make_uint4(0, 0, 0, 0);
-    v[i][1] = r < end ? src[1] : make_uint4(0, 0, 0, 0);
+    const int r = r0 + 2 * i;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + r) * kHeadDim + 16 * part);
+    v[i][0] = r < rows ? src[0] : make_uint4(0, 0, 0, 0);
+    v[i][1] = r < rows ? src[1] : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < kRowsWarp / 2; ++i) {
@@ -1084,6 +1086,8 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     float next_mul = mul0;
     // keys this row's token sees: positions below lim
     const int lim = it.p0 + min(tok, it.ntok - 1) + 1;
+    // (the same for the whole warp)
+    const bool real = tok < it.ntok;
     float m = -INFINITY, base = 0.f, l = 0.f;  // m: raw; base = m mul (0 while m is -inf)
     const float thr_step = C::kRescale / mul;
     float thr = -INFINITY;
@@ -1095,6 +1099,20 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
       const uint32_t sa = tmem + lane_addr + kTmemS + kBlock * j;
       mbar_wait(&S.s_full[j], ((gt + t) >> 1) & 1, abort);
       tc_fence_after();
+      if (!real) {
+        // rows of tokens that the tile lacks: weights of zero. (Their Q is zero too: products of
+        // zeros cost a fraction of the power, and decoding steps, three of four rows of which
+        // are such, ran at 1.6 GHz under the power limit without this.)
+        uint32_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0u;
+        tmem_st_32x32b_x32(sa + 32 * half, z);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive(p_bar[j]);
+        continue;
+      }
       float s[64];
       {
         uint32_t r0[32], r1[32];
@@ -1225,7 +1243,6 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
     // (volatile: written by the other CTA too)
     const uint32_t bad = *static_cast<volatile uint32_t*>(&S.bad[item & 1][half]);
     if (bad != 0) add_late<kFp8>(a, it, bad, tok, head, half, base - C::kPExp, o_addr);
-    const bool real = tok < it.ntok;  // (the same for the whole warp)
     const int slot = 2 * g + (it.blk0 == 0 ? 1 : 0);
     if (whole) {
       // rounded into the ring, as boxes of [128 rows x 64 dimensions] with 128-byte swizzle,

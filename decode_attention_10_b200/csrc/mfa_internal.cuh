@@ -310,8 +310,8 @@ struct ChunkAttnArgs {
   uint32_t* err;
   int pairs;                // CTA pairs of the grid
 };
-// q_map and out_map cover q and out as [n_rows * 64 rows, 256] bf16, boxes of [128 rows x 64
-// dims] and of [64 x 64], 128-byte swizzle.
+// q_map and out_map cover q and out as [n_rows * 64 rows, 256] bf16, boxes of [64 rows x 64
+// dims], 128-byte swizzle.
 cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const CUtensorMap& out_map,
                               const ChunkAttnArgs& a, cudaStream_t s);
 // CTA pairs that can be resident on the current device at once (0 on an error).
