@@ -76,7 +76,6 @@ struct Cfg {
   static constexpr int kVSlots = kFp8 ? 1 : 2;
   static constexpr float kRescale = kFp8 ? 4.0f : 8.0f;  // log2 units
   static constexpr float kPExp = kFp8 ? 4.0f : 0.0f;     // P = 2^(s - m + kPExp)
-  static constexpr int kPolyEvery = 4;  // pairs of weights per pair by polynomial
   static constexpr uint32_t kIdescS = idesc_f16(256, kBlock, !kFp8, false, false);
   static constexpr uint32_t kIdescPV = idesc_f16(256, kHeadDim, !kFp8, false, true);
 };
@@ -786,8 +785,8 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The larger of three, NaN if one is: a row with a NaN score gets a NaN maximum, so every
-// weight of it is NaN (the polynomial below would lose it).
+// The largest of three, NaN if one is: a row with a NaN score has a NaN maximum, and every
+// weight of it is NaN.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -812,28 +811,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-
-// 2^x of two values without the special-function unit, which the softmax keeps busy for as long
-// as one of the two products of a block takes (64 weights a thread, 16 a cycle and SM): x = n + f
-// with n the nearest whole number (added to and taken from 1.5 x 2^23), 2^f for |f| <= 1/2 by a
-// cubic with p(0) = 1 fitted for the least largest relative error (1.0e-4, a twentieth of the
-// bf16 rounding that follows), n added to the exponent. x <= 8; below -127 it gives 0.
-__device__ __forceinline__ void exp2_poly2(uint64_t x, float& y0, float& y1) {
-  float x0, x1;
-  unpair_f32(x, x0, x1);
-  x = pair_f32(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-  const uint64_t t = add2(x, pair_f32(12582912.f, 12582912.f));
-  const uint64_t n = add2(t, pair_f32(-12582912.f, -12582912.f));
-  const uint64_t f = fma2(n, pair_f32(-1.f, -1.f), x);
-  uint64_t p = fma2(pair_f32(0.05500893f, 0.05500893f), f, pair_f32(0.24221096f, 0.24221096f));
-  p = fma2(p, f, pair_f32(0.69328293f, 0.69328293f));
-  p = fma2(p, f, pair_f32(1.f, 1.f));
-  float t0, t1, p0, p1;
-  unpair_f32(t, t0, t1);
-  unpair_f32(p, p0, p1);
-  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
 // f16x2 as e4m3 high and low parts: hi = e4m3(v), lo = e4m3(v - hi) (exact difference)
@@ -1172,8 +1149,10 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
           }
         }
       }
-      // weights 2^(s - base), one of kPolyEvery pairs by polynomial; a hidden key's score is
-      // -inf and its weight 0
+      // weights 2^(s - base); a hidden key's score is -inf and its weight 0. All exponentials go
+      // through the special-function unit, which they keep busy for half of a block's products:
+      // a quarter of them by polynomial made the softmax shorter and long calls 2 to 4 %
+      // slower, since those run at the power limit and the polynomial takes more of it.
       const uint64_t mul2 = pair_f32(mul, mul), off2 = pair_f32(C::kPExp - base, C::kPExp - base);
       uint32_t pw[32];
       uint64_t l2 = pair_f32(0.f, 0.f);
@@ -1181,13 +1160,9 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
       for (int i = 0; i < 32; ++i) {
         const uint64_t x = fma2(pair_f32(s[2 * i], s[2 * i + 1]), mul2, off2);
         float p0, p1;
-        if (i % C::kPolyEvery == C::kPolyEvery - 1) {
-          exp2_poly2(x, p0, p1);
-        } else {
-          unpair_f32(x, p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-        }
+        unpair_f32(x, p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
         l2 = add2(l2, pair_f32(p0, p1));
         pw[i] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
       }
