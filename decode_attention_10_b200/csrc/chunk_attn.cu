@@ -36,7 +36,9 @@
 // kTileCost; pair g takes the g-th of G equal contiguous ranges, so causal chunks, prompts
 // and decoding sequences balance to within a block whatever the mix. A range that starts or
 // ends inside a tile leaves (m, l, O) partials in one of the pair's two slots, merged in a
-// fixed order by chunk_combine_kernel.
+// fixed order by chunk_combine_kernel. Where there are fewer tiles than pairs, each tile is
+// instead cut evenly among pairs of its own if that is about as short: half as many partials,
+// and no pair has two items (32 sequences of 4096 and 4 tokens: 47.5 -> SHARED us).
 //
 // Blocks that hold keys some token of the tile does not see are "special": at most the last
 // two of a tile. Their scores are masked by selection, so nothing a hidden key holds reaches a
@@ -68,6 +70,8 @@ constexpr int kThreads = 32 * (kHelperWarp + 1);
 constexpr int kStageSlots = 4;  // ring slots that a finished tile's 128 x 256 bf16 results take
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
 constexpr int kTileCost = 3;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
+constexpr int kPartCost = 2;  // what a second part in a pair costs over a tile's start, in blocks
+constexpr int kMaxShared = 128;  // (pairs of SMs, at most)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
@@ -83,9 +87,14 @@ struct Cfg {
 struct Plan {
   int32_t cost[kMaxBatch + 1];   // exclusive prefix of the sequences' costs
   int32_t start[kMaxBatch + 1];  // q_start
-  int32_t len[kMaxBatch];        // seq_lens; -1: refused
+  int32_t len[kMaxBatch];        // seq_lens; -1: refused, its rows get zeros
   const int32_t* pages;          // paged: the page table, `page_stride` entries a sequence
   int32_t page_stride;
+  // few tiles (see share_tiles): this pair's part of one
+  int32_t shared;                // 1: the split is of this kind
+  int32_t own_b, own_tile, own_blk0, own_blk1, own_parts;
+  int32_t tile_id[kMaxShared];   // of every tile: sequence and index in it, and blocks
+  int32_t tile_blk[kMaxShared];
 };
 
 struct __align__(1024) Smem {
@@ -325,7 +334,7 @@ static_assert(kTokens == 4 && kBlock == 128, "block_sum's closed form");
 // holds unit t. (total is below 2^30: at most 2^20 + 2^10 tiles of at most 513 + kTileCost
 // units.)
 __device__ __forceinline__ int range_of(int t, int G, int total) {
-  const int q = total / G, r = total % G, cut = r * (q + 1);
+  const int q = total / G, r = total - q * G, cut = r * (q + 1);
   return t < cut ? t / (q + 1) : r + (t - cut) / q;
 }
 static_assert((MFA_MAX_ROWS / kTokens + kMaxBatch) * (int64_t)(MFA_MAX_CONTEXT / kBlock + 1 + kTileCost) <
@@ -339,7 +348,7 @@ struct Item {
   int p0;         // position of the first
   int blk0, blk1; // blocks of this item
   int nblk;       // blocks of the tile
-  int cost0;      // the tile's first unit
+  int parts;      // items of the tile, where this is the first of several
   __device__ int kend() const { return p0 + ntok; }          // one past the last key seen
   __device__ int special() const { return (p0 + 1) / kBlock; }  // first special block
   __device__ bool whole() const { return blk0 == 0 && blk1 == nblk; }
@@ -347,14 +356,22 @@ struct Item {
 
 struct Cursor {
   const Plan* P;
-  int batch, begin, end, pos, b, tile;
+  int batch, g, G, total, begin, end, pos, b, tile;
 
   // Called by whole warps: each search looks at 32 places a step.
-  __device__ void init(const Plan& plan, int batch_, int g, int G) {
+  __device__ void init(const Plan& plan, int batch_, int g_, int G_) {
     P = &plan;
     batch = batch_;
-    const int total = plan.cost[batch];
+    g = g_;
+    G = G_;
+    total = plan.cost[batch];
     begin = end = pos = b = tile = 0;
+    if (plan.shared) {
+      b = plan.own_b;
+      tile = plan.own_tile;
+      end = plan.own_blk1 > plan.own_blk0;
+      return;
+    }
     if (total == 0 || g >= G) return;
     const int q = total / G, r = total - q * G;
     begin = g * q + min(g, r);
@@ -379,20 +396,37 @@ struct Cursor {
     }
   }
 
+  // The tile `tile` of sequence b.
+  __device__ void describe(Item& it) const {
+    const int n = P->start[b + 1] - P->start[b];
+    it.b = b;
+    it.ntok = min(kTokens, n - kTokens * tile);
+    it.row0 = P->start[b] + kTokens * tile;
+    it.p0 = P->len[b] - n + kTokens * tile;
+    it.nblk = (it.kend() + kBlock - 1) / kBlock;
+    it.parts = 0;
+  }
+
   __device__ bool next(Item& it) {
+    if (P->shared) {
+      if (pos >= end) return false;
+      pos = end;
+      describe(it);
+      it.blk0 = P->own_blk0;
+      it.blk1 = P->own_blk1;
+      it.parts = P->own_parts;
+      return true;
+    }
     while (pos < end) {
-      const int n = P->start[b + 1] - P->start[b];
-      it.b = b;
-      it.ntok = min(kTokens, n - kTokens * tile);
-      it.row0 = P->start[b] + kTokens * tile;
-      it.p0 = P->len[b] - n + kTokens * tile;
-      it.nblk = (it.kend() + kBlock - 1) / kBlock;
-      it.cost0 = pos;
-      it.blk0 = max(0, begin - pos - kTileCost);
-      it.blk1 = min(it.nblk, end - pos - kTileCost);
-      pos += kTileCost + it.nblk;
+      describe(it);
+      const int first = pos + kTileCost;  // the tile's first block
+      it.blk0 = max(0, begin - first);
+      it.blk1 = min(it.nblk, end - first);
+      if (it.blk0 == 0 && it.blk1 > 0 && it.blk1 < it.nblk)
+        it.parts = range_of(first + it.nblk - 1, G, total) - g + 1;
+      pos = first + it.nblk;
       ++tile;
-      if (kTokens * tile >= n) {
+      if (kTokens * tile >= P->start[b + 1] - P->start[b]) {
         tile = 0;
         do ++b; while (b < batch && P->cost[b + 1] == P->cost[b]);
       }
@@ -402,9 +436,71 @@ struct Cursor {
   }
 };
 
-// Every thread of the CTA: the sequences' costs, from the lengths on the device. Refused
-// sequences cost nothing (len -1) and, if `report`, are flagged.
-__device__ void build_plan(Smem& S, const ChunkAttnArgs& a, bool report) {
+// Warp 0, when there are no more tiles than pairs: the least M for which cutting every tile into
+// ceil(blocks / M) even parts takes no more parts than pairs, and this pair's part. Taken if
+// the longest part is about as short as a range of the other kind, whose pairs have two parts
+// each. (t0: this lane's first tile, of its run of sequences [b0, b1).)
+__device__ __forceinline__ void share_tiles(Plan& P, int tiles, int t0, int b0, int b1, int batch, int g,
+                                            int pairs) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = kMaxShared / 32;
+  for (int b = b0; b < b1; ++b) {
+    if (P.cost[b + 1] == P.cost[b]) continue;
+    const int n = P.start[b + 1] - P.start[b], p = P.len[b] - n;
+    for (int i = 0; kTokens * i < n; ++i, ++t0) {
+      P.tile_id[t0] = b * kMaxShared + i;
+      P.tile_blk[t0] = (p + min(n, kTokens * (i + 1)) + kBlock - 1) / kBlock;
+    }
+  }
+  __syncwarp();
+  int blk[kPer], k[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) blk[j] = kPer * lane + j < tiles ? P.tile_blk[kPer * lane + j] : 0;
+  const int total = P.cost[batch], most = (total + pairs - 1) / pairs + kPartCost;
+  int M = (total - tiles * kTileCost + pairs - 1) / pairs, sum = 0;
+  for (;; ++M) {
+    if (M > most) return;
+    const float r = 1.f / M;
+    sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      // ceil(blk / M), exact: both are below 1024, so the quotient is 2^-11 from a whole number
+      k[j] = static_cast<int>((blk[j] + M - 1 + 0.5f) * r);
+      sum += k[j];
+    }
+    if (__reduce_add_sync(0xffffffffu, sum) <= pairs) break;
+  }
+  int first = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, first, o);
+    if (lane >= o) first += y;
+  }
+  first -= sum;
+  if (lane == 0) {
+    P.shared = 1;
+    P.own_blk0 = P.own_blk1 = 0;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int part = g - first;
+    if (part >= 0 && part < k[j]) {
+      const int id = P.tile_id[kPer * lane + j];
+      P.own_b = id / kMaxShared;
+      P.own_tile = id % kMaxShared;
+      P.own_blk0 = part * blk[j] / k[j];
+      P.own_blk1 = (part + 1) * blk[j] / k[j];
+      P.own_parts = k[j];
+    }
+    first += k[j];
+  }
+}
+
+// Every thread of the CTA: the sequences' costs, from the lengths on the device, and the split.
+// Refused sequences cost nothing (len -1) and, if `report`, are flagged; a table or ranges of
+// rows that do not hold together refuse all.
+__device__ void build_plan(Smem& S, const ChunkAttnArgs& a, int g, int pairs, bool report) {
   Plan& P = S.plan;
   uint32_t bits = 0;
   if (threadIdx.x == kThreads - 1) {
@@ -416,12 +512,8 @@ __device__ void build_plan(Smem& S, const ChunkAttnArgs& a, bool report) {
     const int s0 = a.q_start[b], s1 = a.q_start[b + 1], L = a.seq_lens[b];
     const KvSeq& kv = a.kv[b];
     int cost = 0, len = L;
-    if (kv.chunk_maps == 0 || kv.page_size != a.page_size) {
+    if (kv.chunk_maps == 0 || kv.page_size != a.page_size || s0 < 0 || s1 < s0 || s1 > a.n_rows) {
       bits |= kErrLayout;
-      len = -2;  // nothing at all is computed
-    } else if (s0 < 0 || s1 < s0 || s1 > a.n_rows) {
-      bits |= kErrLayout;
-      len = -2;  // no rows to speak of
     } else if (s1 > s0) {
       if (L > kv.capacity) {
         bits |= kErrCapacity;
@@ -439,18 +531,22 @@ __device__ void build_plan(Smem& S, const ChunkAttnArgs& a, bool report) {
     if (b == a.batch - 1) P.start[a.batch] = s1;
   }
   if (report && bits != 0) atomicOr(a.err, bits);
-  __syncthreads();
+  const bool none = __syncthreads_or(bits & kErrLayout);
   // exclusive prefix: warp 0, each lane a run of sequences
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (a.batch + 31) / 32;
     const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += P.cost[b];
-    int incl = sum;
+    int sum = 0, tiles = 0;
+    for (int b = b0; b < b1; ++b) {
+      if (none) P.cost[b] = 0, P.len[b] = -2;
+      sum += P.cost[b];
+      if (P.cost[b] != 0) tiles += (P.start[b + 1] - P.start[b] + kTokens - 1) / kTokens;
+    }
+    int incl = sum, tincl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, tincl, o);
+      if (lane >= o) incl += y, tincl += z;
     }
     int run = incl - sum;
     for (int b = b0; b < b1; ++b) {
@@ -459,6 +555,11 @@ __device__ void build_plan(Smem& S, const ChunkAttnArgs& a, bool report) {
       run += c;
     }
     if (lane == 31) P.cost[a.batch] = incl;
+    if (lane == 0) P.shared = 0;
+    __syncwarp();
+    const int all = __shfl_sync(0xffffffffu, tincl, 31);
+    if (all > 0 && all <= min(pairs, kMaxShared))
+      share_tiles(P, all, tincl - tiles, b0, b1, a.batch, g, pairs);
   }
   __syncthreads();
 }
@@ -522,12 +623,12 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   cur.init(S.plan, a.batch, g, G);
   Item it, nx;
   bool has = cur.next(it);
-  if (has && leader) {
+  if (!kPaged && has && leader) {
     prefetch_tensormap(&maps[it.b].k);
     prefetch_tensormap(&maps[it.b].v);
   }
   while (has) {
-    const KvChunkMaps* map = maps + it.b;
+    const KvChunkMaps* map = kPaged ? maps : maps + it.b;  // (one pool)
     const bool has_nx = cur.next(nx);
     if constexpr (!kFp8) {
       if (item > 0) mbar_wait(&S.q_empty, (item - 1) & 1, abort);
@@ -625,8 +726,10 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
       // the next item's Q (read once from HBM) on its way to L2, and its tensor maps
       for (int tok = kCtaTokens * rank; tok < min(kCtaTokens * static_cast<int>(rank + 1), nx.ntok); ++tok)
         for (int c = 0; c < 4; ++c) tma_prefetch_2d(q_map, 64 * c, (nx.row0 + tok) * kHeads);
-      prefetch_tensormap(&maps[nx.b].k);
-      prefetch_tensormap(&maps[nx.b].v);
+      if constexpr (!kPaged) {
+        prefetch_tensormap(&maps[nx.b].k);
+        prefetch_tensormap(&maps[nx.b].v);
+      }
     }
     for (int blk = it.blk0; blk < it.blk1; ++blk) {
       if (blk + 1 < it.blk1) load_k(blk + 1);
@@ -1277,11 +1380,7 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
         slot_m(a.partials, slot)[rank * kRows + row] = m == -INFINITY ? -INFINITY : base;
         slot_l(a.partials, slot)[rank * kRows + row] = l;
       }
-      if (it.blk0 == 0) {
-        const int total = S.plan.cost[a.batch];
-        const int last = range_of(it.cost0 + kTileCost + it.nblk - 1, G, total);
-        info = make_int2(it.row0, (last - g + 1) * 8 + it.ntok);
-      }
+      if (it.blk0 == 0) info = make_int2(it.row0, it.parts * 8 + it.ntok);
     }
     if (bad != 0) {
       // the flag is spent: back to 0 once both halves' warps of this CTA have read it
@@ -1406,6 +1505,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&out_map);
+    if (kPaged) {  // (the table is the host's; no kernel writes it)
+      const KvChunkMaps* maps = reinterpret_cast<const KvChunkMaps*>(a.kv + a.batch);
+      prefetch_tensormap(&maps->k);
+      prefetch_tensormap(&maps->v);
+    }
   }
   if (warp == 1) pair_tmem_alloc(&S.tmem_base);
   tc_fence_before();
@@ -1413,7 +1517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_arrive();  // this CTA's barriers are set up
   pdl_launch_dependents();
   pdl_wait();
-  build_plan(S, a, blockIdx.x == 0);
+  build_plan(S, a, g, static_cast<int>(gridDim.x) / 2, blockIdx.x == 0);
   const int G = min(static_cast<int>(gridDim.x) / 2, S.plan.cost[a.batch]);
   cluster_wait();  // and the other's
   tc_fence_after();

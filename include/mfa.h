@@ -338,11 +338,11 @@ MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, c
  * q: device bf16 [n_rows, 64, 256]; out: device bf16 [n_rows, 64, 256]; scale > 0.
  * kv: a table of mfa_chunk_table_bytes(kv->batch) bytes or more.
  * ws: device workspace of mfa_chunk_workspace_bytes(kv->batch) bytes (initialized once).
- * A sequence with seq_lens[b] > capacity[b] (MFA_ERR_CAPACITY), with 0 <= seq_lens[b] < n_b
- * (MFA_ERR_EMPTY: a token without positions), or with q_start[b] .. q_start[b + 1] not a
- * range of [0, n_rows) (MFA_ERR_INVALID_ARG) is not computed; its rows of out, where it has
- * any, are zero-filled. A table without the chunk attention's maps, or of another layout than
- * kv->page_size, leaves out untouched and sets MFA_ERR_INVALID_ARG. */
+ * A sequence with new tokens and seq_lens[b] > capacity[b] (MFA_ERR_CAPACITY) or seq_lens[b] <
+ * n_b (MFA_ERR_EMPTY: a token without positions) is not computed; its rows of out are
+ * zero-filled. A q_start that is not nondecreasing within [0, n_rows], a table without the
+ * chunk attention's maps or of another layout than kv->page_size: nothing is computed, out
+ * stays as it was, and MFA_ERR_INVALID_ARG is set. */
 MFA_API mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* q_start,
                                   const int32_t* seq_lens, int32_t n_rows, float scale,
                                   void* out, void* ws, size_t ws_bytes, void* stream);

@@ -224,12 +224,12 @@ def test_errors_are_reported_and_zero_filled():
         assert mfa.get_error(ws) == 6
         assert (out[5:9] == 0).all()
         assert torch.equal(out[:5], good[:5]) and torch.equal(out[9:], good[9:])
-    # ranges outside the rows: not computed, nothing written outside `out`
+    # ranges that do not hold together: nothing is computed
     for starts in ([0, 2, 5, 9, 40], [-3, 2, 5, 9, 11], [0, 2, 1, 4, 11], [0, 2, 5, 900, 11]):
         out = torch.full_like(b.q, 5.0)
         q_start = torch.tensor(starts, dtype=torch.int32, device="cuda")
         mfa.chunk_attn(b.q, cache, q_start, b.seq_lens, out=out, ws=ws)
-        assert mfa.get_error(ws) == 1
+        assert mfa.get_error(ws) == 1 and (out == 5.0).all()
     out = torch.full_like(b.q, 5.0)
     mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, out=out, ws=ws)
     assert mfa.get_error(ws) == 0 and torch.equal(out, good)
