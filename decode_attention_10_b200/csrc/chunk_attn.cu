@@ -90,11 +90,12 @@ struct Plan {
   int32_t len[kMaxBatch];        // seq_lens; -1: refused, its rows get zeros
   const int32_t* pages;          // paged: the page table, `page_stride` entries a sequence
   int32_t page_stride;
-  // few tiles (see share_tiles): this pair's part of one
-  int32_t shared;                // 1: the split is of this kind
-  int32_t own_b, own_tile, own_blk0, own_blk1, own_parts;
-  int32_t tile_id[kMaxShared];   // of every tile: sequence and index in it, and blocks
-  int32_t tile_blk[kMaxShared];
+  // this pair's share: units [begin, end), the first of them in tile `tile` of sequence b, which
+  // begins at unit pos; or (shared, see share_tiles) blocks [begin, end) of that tile alone,
+  // one of `parts`
+  int32_t begin, end, pos, b, tile, shared, parts;
+  int32_t pairs;                 // pairs with a share
+  int32_t tile_blk[kMaxShared];  // share_tiles: every tile's blocks
 };
 
 struct __align__(1024) Smem {
@@ -354,46 +355,34 @@ struct Item {
   __device__ bool whole() const { return blk0 == 0 && blk1 == nblk; }
 };
 
+// The last i of [0, n) with pred(i), which holds from 0 up to some i; by a whole warp, which
+// looks at 32 places a step.
+template <class F>
+__device__ __forceinline__ int last_true(int n, F&& pred) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  for (int step = n > 1024 ? 1024 : n > 32 ? 32 : 1;; step /= 32) {
+    const int i = lo + lane * step;
+    const uint32_t yes = __ballot_sync(0xffffffffu, i < n && pred(i));
+    lo += (31 - __clz(yes)) * step;  // (lane 0 says yes)
+    if (step == 1) return lo;
+  }
+}
+
+// A pair's items, in order.
 struct Cursor {
   const Plan* P;
-  int batch, g, G, total, begin, end, pos, b, tile;
+  int batch, g, begin, end, pos, b, tile;
 
-  // Called by whole warps: each search looks at 32 places a step.
-  __device__ void init(const Plan& plan, int batch_, int g_, int G_) {
+  __device__ void init(const Plan& plan, int batch_, int g_) {
     P = &plan;
     batch = batch_;
     g = g_;
-    G = G_;
-    total = plan.cost[batch];
-    begin = end = pos = b = tile = 0;
-    if (plan.shared) {
-      b = plan.own_b;
-      tile = plan.own_tile;
-      end = plan.own_blk1 > plan.own_blk0;
-      return;
-    }
-    if (total == 0 || g >= G) return;
-    const int q = total / G, r = total - q * G;
-    begin = g * q + min(g, r);
-    end = begin + q + (g < r);
-    // the sequence, then the tile, that hold unit `begin`: the last that starts at or before it
-    b = last_true(batch, [&](int i) { return plan.cost[i] <= begin; });
-    const int n = plan.start[b + 1] - plan.start[b], p = plan.len[b] - n, c = plan.cost[b];
-    tile = last_true((n + kTokens - 1) / kTokens, [&](int i) { return c + tile_offset(p, i) <= begin; });
-    pos = c + tile_offset(p, tile);
-  }
-
-  // The last i of [0, n) with pred(i), which holds from 0 up to some i.
-  template <class F>
-  static __device__ int last_true(int n, F&& pred) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0;  // pred(lo) holds
-    for (int step = n > 1024 ? 1024 : n > 32 ? 32 : 1;; step /= 32) {
-      const int i = lo + lane * step;
-      const uint32_t yes = __ballot_sync(0xffffffffu, i < n && pred(i));
-      lo += (31 - __clz(yes)) * step;  // (lane 0 says yes)
-      if (step == 1) return lo;
-    }
+    begin = plan.begin;
+    end = plan.end;
+    pos = plan.pos;
+    b = plan.b;
+    tile = plan.tile;
   }
 
   // The tile `tile` of sequence b.
@@ -409,12 +398,12 @@ struct Cursor {
 
   __device__ bool next(Item& it) {
     if (P->shared) {
-      if (pos >= end) return false;
-      pos = end;
+      if (begin >= end) return false;
       describe(it);
-      it.blk0 = P->own_blk0;
-      it.blk1 = P->own_blk1;
-      it.parts = P->own_parts;
+      it.blk0 = begin;
+      it.blk1 = end;
+      it.parts = P->parts;
+      begin = end;
       return true;
     }
     while (pos < end) {
@@ -423,7 +412,7 @@ struct Cursor {
       it.blk0 = max(0, begin - first);
       it.blk1 = min(it.nblk, end - first);
       if (it.blk0 == 0 && it.blk1 > 0 && it.blk1 < it.nblk)
-        it.parts = range_of(first + it.nblk - 1, G, total) - g + 1;
+        it.parts = range_of(first + it.nblk - 1, P->pairs, P->cost[batch]) - g + 1;
       pos = first + it.nblk;
       ++tile;
       if (kTokens * tile >= P->start[b + 1] - P->start[b]) {
@@ -439,69 +428,121 @@ struct Cursor {
 // Warp 0, when there are no more tiles than pairs: the least M for which cutting every tile into
 // ceil(blocks / M) even parts takes no more parts than pairs, and this pair's part. Taken if
 // the longest part is about as short as a range of the other kind, whose pairs have two parts
-// each. (t0: this lane's first tile, of its run of sequences [b0, b1).)
-__device__ __forceinline__ void share_tiles(Plan& P, int tiles, int t0, int b0, int b1, int batch, int g,
-                                            int pairs) {
+// each. (Each lane has a run of sequences [b0, b1) with `mine` tiles from t0 on, of lo .. hi
+// blocks.)
+__device__ __forceinline__ bool share_tiles(Plan& P, int tiles, int t0, int mine, int lo, int hi, int b0,
+                                            int b1, int batch, int g, int pairs) {
   const int lane = threadIdx.x & 31;
-  constexpr int kPer = kMaxShared / 32;
-  for (int b = b0; b < b1; ++b) {
-    if (P.cost[b + 1] == P.cost[b]) continue;
-    const int n = P.start[b + 1] - P.start[b], p = P.len[b] - n;
-    for (int i = 0; kTokens * i < n; ++i, ++t0) {
-      P.tile_id[t0] = b * kMaxShared + i;
-      P.tile_blk[t0] = (p + min(n, kTokens * (i + 1)) + kBlock - 1) / kBlock;
-    }
-  }
-  __syncwarp();
-  int blk[kPer], k[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) blk[j] = kPer * lane + j < tiles ? P.tile_blk[kPer * lane + j] : 0;
   const int total = P.cost[batch], most = (total + pairs - 1) / pairs + kPartCost;
-  int M = (total - tiles * kTileCost + pairs - 1) / pairs, sum = 0;
-  for (;; ++M) {
-    if (M > most) return;
-    const float r = 1.f / M;
-    sum = 0;
+  lo = __reduce_min_sync(0xffffffffu, mine > 0 ? lo : 1 << 30);
+  hi = __reduce_max_sync(0xffffffffu, mine > 0 ? hi : 0);
+  int tile, part, k, blk = hi;
+  if (lo == hi) {  // all alike (decoding, or one tile): no search
+    const int split = min(pairs / tiles, hi);
+    const int M = (hi + split - 1) / split;
+    if (M > most) return false;
+    k = (hi + M - 1) / M;
+    tile = g / k;
+    part = g - tile * k;
+  } else {
+    constexpr int kPer = kMaxShared / 32;
+    for (int b = b0, t = t0; b < b1; ++b) {
+      if (P.cost[b + 1] == P.cost[b]) continue;
+      const int n = P.start[b + 1] - P.start[b], p = P.len[b] - n;
+      for (int i = 0; kTokens * i < n; ++i, ++t)
+        P.tile_blk[t] = (p + min(n, kTokens * (i + 1)) + kBlock - 1) / kBlock;
+    }
+    __syncwarp();
+    int c[kPer], ks[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) c[j] = kPer * lane + j < tiles ? P.tile_blk[kPer * lane + j] : 0;
+    int M = (total - tiles * kTileCost + pairs - 1) / pairs, sum = 0;
+    for (;; ++M) {
+      if (M > most) return false;
+      const float r = 1.f / M;
+      sum = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        // ceil(c / M), exact: both are below 1024, so the quotient is 2^-11 from a whole number
+        ks[j] = static_cast<int>((c[j] + M - 1 + 0.5f) * r);
+        sum += ks[j];
+      }
+      if (__reduce_add_sync(0xffffffffu, sum) <= pairs) break;
+    }
+    int first = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, first, o);
+      if (lane >= o) first += y;
+    }
+    first -= sum;
+    int found = -1;
+    tile = tiles, part = 0, k = 1;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      // ceil(blk / M), exact: both are below 1024, so the quotient is 2^-11 from a whole number
-      k[j] = static_cast<int>((blk[j] + M - 1 + 0.5f) * r);
-      sum += k[j];
+      if (g >= first && g < first + ks[j]) {
+        found = kPer * lane + j;
+        part = g - first;
+        k = ks[j];
+        blk = c[j];
+      }
+      first += ks[j];
     }
-    if (__reduce_add_sync(0xffffffffu, sum) <= pairs) break;
+    const uint32_t who = __ballot_sync(0xffffffffu, found >= 0);
+    if (who != 0) {
+      const int l = __ffs(who) - 1;
+      tile = __shfl_sync(0xffffffffu, found, l);
+      part = __shfl_sync(0xffffffffu, part, l);
+      k = __shfl_sync(0xffffffffu, k, l);
+      blk = __shfl_sync(0xffffffffu, blk, l);
+    }
   }
-  int first = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, first, o);
-    if (lane >= o) first += y;
-  }
-  first -= sum;
   if (lane == 0) {
     P.shared = 1;
-    P.own_blk0 = P.own_blk1 = 0;
+    P.begin = P.end = 0;
+    P.b = P.tile = 0;
+    P.parts = k;
   }
   __syncwarp();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int part = g - first;
-    if (part >= 0 && part < k[j]) {
-      const int id = P.tile_id[kPer * lane + j];
-      P.own_b = id / kMaxShared;
-      P.own_tile = id % kMaxShared;
-      P.own_blk0 = part * blk[j] / k[j];
-      P.own_blk1 = (part + 1) * blk[j] / k[j];
-      P.own_parts = k[j];
+  if (tile >= t0 && tile < t0 + mine) {  // the lane whose sequences it is in
+    int t = tile - t0, b = b0;
+    for (;; ++b) {
+      const int n = P.cost[b + 1] != P.cost[b] ? (P.start[b + 1] - P.start[b] + kTokens - 1) / kTokens : 0;
+      if (t < n) break;
+      t -= n;
     }
-    first += k[j];
+    P.b = b;
+    P.tile = t;
+    P.begin = part * blk / k;
+    P.end = (part + 1) * blk / k;
   }
+  return true;
 }
 
-// Every thread of the CTA: the sequences' costs, from the lengths on the device, and the split.
-// Refused sequences cost nothing (len -1) and, if `report`, are flagged; a table or ranges of
-// rows that do not hold together refuse all.
-__device__ void build_plan(Smem& S, const ChunkAttnArgs& a, int g, int pairs, bool report) {
+// What is asked of sequence b: its range of rows, its length (-1: refused, its rows get zeros) and
+// its cost; the returned bits say why it is refused. A table or ranges of rows that do not hold
+// together (kErrLayout) refuse all.
+__device__ __forceinline__ uint32_t read_sequence(const ChunkAttnArgs& a, int b, int& s0, int& s1, int& len,
+                                                  int& cost) {
+  s0 = a.q_start[b], s1 = a.q_start[b + 1], len = a.seq_lens[b];
+  const KvSeq& kv = a.kv[b];
+  cost = 0;
+  if (kv.chunk_maps == 0 || kv.page_size != a.page_size || s0 < 0 || s1 < s0 || s1 > a.n_rows)
+    return kErrLayout;
+  if (s1 == s0) return 0;
+  const uint32_t bits = len > kv.capacity ? kErrCapacity : len < s1 - s0 ? kErrEmpty : 0u;
+  if (bits != 0)
+    len = -1;
+  else
+    cost = seq_cost(s1 - s0, len);
+  return bits;
+}
+
+// Every thread of the CTA: the sequences, from the lengths on the device, and this pair's share.
+// Up to 32 sequences are read by the lanes of warp 0, which goes on with them.
+__device__ __forceinline__ void build_plan(Smem& S, const ChunkAttnArgs& a, int g, int pairs, bool report) {
   Plan& P = S.plan;
+  const bool few = a.batch <= 32;
   uint32_t bits = 0;
   if (threadIdx.x == kThreads - 1) {
     // (rows of one table, a fixed distance apart)
@@ -509,44 +550,39 @@ __device__ void build_plan(Smem& S, const ChunkAttnArgs& a, int g, int pairs, bo
     P.page_stride = a.batch > 1 ? static_cast<int>(a.kv[1].pages - a.kv[0].pages) : 0;
   }
   for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], L = a.seq_lens[b];
-    const KvSeq& kv = a.kv[b];
-    int cost = 0, len = L;
-    if (kv.chunk_maps == 0 || kv.page_size != a.page_size || s0 < 0 || s1 < s0 || s1 > a.n_rows) {
-      bits |= kErrLayout;
-    } else if (s1 > s0) {
-      if (L > kv.capacity) {
-        bits |= kErrCapacity;
-        len = -1;
-      } else if (L < s1 - s0) {
-        bits |= kErrEmpty;
-        len = -1;
-      } else {
-        cost = seq_cost(s1 - s0, L);
-      }
-    }
+    int s0, s1, len, cost;
+    bits |= read_sequence(a, b, s0, s1, len, cost);
     P.start[b] = s0;
     P.len[b] = len;
     P.cost[b] = cost;
     if (b == a.batch - 1) P.start[a.batch] = s1;
   }
   if (report && bits != 0) atomicOr(a.err, bits);
-  const bool none = __syncthreads_or(bits & kErrLayout);
-  // exclusive prefix: warp 0, each lane a run of sequences
+  const bool none = few ? __any_sync(0xffffffffu, (bits & kErrLayout) != 0)
+                        : __syncthreads_or(bits & kErrLayout) != 0;
   if (threadIdx.x < 32) {
+    // exclusive prefix of the costs, each lane a run of sequences
     const int lane = threadIdx.x, per = (a.batch + 31) / 32;
     const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
-    int sum = 0, tiles = 0;
+    __syncwarp();
+    int sum = 0, mine = 0, lo = 1 << 30, hi = 0;
     for (int b = b0; b < b1; ++b) {
       if (none) P.cost[b] = 0, P.len[b] = -2;
-      sum += P.cost[b];
-      if (P.cost[b] != 0) tiles += (P.start[b + 1] - P.start[b] + kTokens - 1) / kTokens;
+      const int c = P.cost[b];
+      sum += c;
+      if (c != 0) {
+        // (blocks of a sequence's first and last tile: the least and the most of its tiles)
+        const int n = P.start[b + 1] - P.start[b], len = P.len[b];
+        mine += (n + kTokens - 1) / kTokens;
+        lo = min(lo, (len - n + min(n, kTokens) + kBlock - 1) / kBlock);
+        hi = max(hi, (len + kBlock - 1) / kBlock);
+      }
     }
-    int incl = sum, tincl = tiles;
+    int incl = sum, tiles = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, tincl, o);
-      if (lane >= o) incl += y, tincl += z;
+      const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, tiles, o);
+      if (lane >= o) incl += y, tiles += z;
     }
     int run = incl - sum;
     for (int b = b0; b < b1; ++b) {
@@ -555,11 +591,31 @@ __device__ void build_plan(Smem& S, const ChunkAttnArgs& a, int g, int pairs, bo
       run += c;
     }
     if (lane == 31) P.cost[a.batch] = incl;
-    if (lane == 0) P.shared = 0;
     __syncwarp();
-    const int all = __shfl_sync(0xffffffffu, tincl, 31);
-    if (all > 0 && all <= min(pairs, kMaxShared))
-      share_tiles(P, all, tincl - tiles, b0, b1, a.batch, g, pairs);
+    const int total = P.cost[a.batch], all = __shfl_sync(0xffffffffu, tiles, 31);
+    const bool shared = all > 0 && all <= min(pairs, kMaxShared) &&
+                        share_tiles(P, all, tiles - mine, mine, lo, hi, b0, b1, a.batch, g, pairs);
+    if (!shared) {
+      // range g of G nearly equal ones of all units, the first total mod G one longer
+      const int G = min(pairs, total);
+      int begin = 0, end = 0, b = 0, tile = 0, pos = 0;
+      if (g < G) {
+        const int q = total / G, r = total - q * G;
+        begin = g * q + min(g, r);
+        end = begin + q + (g < r);
+        // the sequence, then the tile, that hold unit `begin`: the last that starts there or before
+        b = last_true(a.batch, [&](int i) { return P.cost[i] <= begin; });
+        const int n = P.start[b + 1] - P.start[b], p = P.len[b] - n, c = P.cost[b];
+        tile = last_true((n + kTokens - 1) / kTokens, [&](int i) { return c + tile_offset(p, i) <= begin; });
+        pos = c + tile_offset(p, tile);
+      }
+      if (lane == 0) {
+        P.begin = begin, P.end = end, P.pos = pos;
+        P.b = b, P.tile = tile;
+        P.pairs = G;
+        P.shared = 0;
+      }
+    }
   }
   __syncthreads();
 }
@@ -608,7 +664,7 @@ struct Groups {
 
 template <bool kFp8, bool kPaged>
 __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnArgs& a, int g,
-                             int G, uint32_t rank) {
+                             uint32_t rank) {
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
   const int lane = threadIdx.x & 31;
@@ -620,7 +676,7 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   uint32_t chunk = 0, issued = 0, specials = 0;
   int item = 0;
   Cursor cur;
-  cur.init(S.plan, a.batch, g, G);
+  cur.init(S.plan, a.batch, g);
   Item it, nx;
   bool has = cur.next(it);
   if (!kPaged && has && leader) {
@@ -764,7 +820,7 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
 // warp 1 of the first CTA: the products
 // ---------------------------------------------------------------------------------------
 template <bool kFp8>
-__device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t tmem) {
+__device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, uint32_t tmem) {
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
   const bool leader = elect_one();
@@ -840,7 +896,7 @@ __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t 
   };
 
   Cursor cur;
-  cur.init(S.plan, a.batch, g, G);
+  cur.init(S.plan, a.batch, g);
   Item it;
   while (cur.next(it)) {
     const int n = it.blk1 - it.blk0;
@@ -1113,7 +1169,7 @@ __device__ __noinline__ void add_late(const ChunkAttnArgs& a, const Item& it, ui
 }
 
 template <bool kFp8>
-__device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint32_t rank,
+__device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t rank,
                             uint32_t tmem) {
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
@@ -1144,7 +1200,7 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
   int2 info = make_int2(0, 0);  // for the combine kernel: rows of the tile and its parts
 
   Cursor cur;
-  cur.init(S.plan, a.batch, g, G);
+  cur.init(S.plan, a.batch, g);
   Item it, nx;
   bool has = cur.next(it);
   float mul = mul0;
@@ -1400,7 +1456,7 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, int G, uint3
 // the helper warp: looks special blocks' V over, stores finished tiles
 // ---------------------------------------------------------------------------------------
 template <bool kFp8>
-__device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnArgs& a, int g, int G,
+__device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnArgs& a, int g,
                            uint32_t rank) {
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
@@ -1409,7 +1465,7 @@ __device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnA
   uint32_t chunk = 0, specials = 0;
   int item = 0, tiles = 0;
   Cursor cur;
-  cur.init(S.plan, a.batch, g, G);
+  cur.init(S.plan, a.batch, g);
   Item it;
   while (cur.next(it)) {
     const int n = it.blk1 - it.blk0;
@@ -1518,19 +1574,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
   build_plan(S, a, g, static_cast<int>(gridDim.x) / 2, blockIdx.x == 0);
-  const int G = min(static_cast<int>(gridDim.x) / 2, S.plan.cost[a.batch]);
   cluster_wait();  // and the other's
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
   if (warp == 0) {
-    run_producer<kFp8, kPaged>(S, &q_map, a, g, G, rank);
+    run_producer<kFp8, kPaged>(S, &q_map, a, g, rank);
   } else if (warp == 1) {
-    if (rank == 0) run_mma<kFp8>(S, a, g, G, tmem);
+    if (rank == 0) run_mma<kFp8>(S, a, g, tmem);
   } else if (warp == kHelperWarp) {
-    run_helper<kFp8>(S, &out_map, a, g, G, rank);
+    run_helper<kFp8>(S, &out_map, a, g, rank);
   } else {
-    run_softmax<kFp8>(S, a, g, G, rank, tmem);
+    run_softmax<kFp8>(S, a, g, rank, tmem);
   }
 
   tc_fence_before();
