@@ -662,6 +662,21 @@ struct Groups {
   }
 };
 
+// bf16: an item's Q, 64 KB a CTA. Tokens that the tile lacks are rows past the end of q, which read
+// as zeros. (One lane.)
+__device__ __forceinline__ void load_q(Smem& S, const CUtensorMap* q_map, const ChunkAttnArgs& a,
+                                       const Item& it, uint32_t rank) {
+  const uint32_t bar = map_to(&S.q_full, 0);
+  const uint64_t once = policy_evict_first();
+  if (rank == 0) mbar_arrive_expect_tx(&S.q_full, 2 * 4 * kQChunkBytes);
+#pragma unroll 1
+  for (int i = 0; i < 4 * kCtaTokens; ++i) {
+    const int k = i / 4, c = i % 4, tok = kCtaTokens * static_cast<int>(rank) + k;
+    const int y = (tok < it.ntok ? it.row0 + tok : a.n_rows) * kHeads;
+    pair_load_2d(S.q + c * kQChunkBytes + k * kHeads * 128, q_map, 64 * c, y, bar, once);
+  }
+}
+
 template <bool kFp8, bool kPaged>
 __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnArgs& a, int g,
                              uint32_t rank) {
@@ -671,7 +686,6 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   const bool leader = elect_one();
   const KvChunkMaps* maps = reinterpret_cast<const KvChunkMaps*>(a.kv + a.batch);
   const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
-  const uint32_t q_bar = map_to(&S.q_full, 0);
   const int page_shift = kPaged ? 31 - __clz(a.page_size) : 0;
   uint32_t chunk = 0, issued = 0, specials = 0;
   int item = 0;
@@ -685,18 +699,10 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   }
   while (has) {
     const KvChunkMaps* map = kPaged ? maps : maps + it.b;  // (one pool)
-    const bool has_nx = cur.next(nx);
     if constexpr (!kFp8) {
-      if (item > 0) mbar_wait(&S.q_empty, (item - 1) & 1, abort);
-      if (leader && !*abort) {
-        if (rank == 0) mbar_arrive_expect_tx(&S.q_full, 2 * 4 * kQChunkBytes);
-        for (int k = 0; k < kCtaTokens; ++k) {
-          // tokens that the tile lacks: rows past the end of q, which read as zeros
-          const int tok = kCtaTokens * static_cast<int>(rank) + k;
-          const int y = (tok < it.ntok ? it.row0 + tok : a.n_rows) * kHeads;
-          for (int c = 0; c < 4; ++c)
-            pair_load_2d(S.q + c * kQChunkBytes + k * kHeads * 128, q_map, 64 * c, y, q_bar, once);
-        }
+      if (item > 0) {  // (the first item's Q is loaded by the helper warp meanwhile)
+        mbar_wait(&S.q_empty, (item - 1) & 1, abort);
+        if (leader && !*abort) load_q(S, q_map, a, it, rank);
       }
     }
     // one tile of the sequence reads its rows once; several find them in L2
@@ -778,6 +784,7 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
       specials += special;
     };
     load_k(it.blk0);
+    const bool has_nx = cur.next(nx);
     if (has_nx && leader) {
       // the next item's Q (read once from HBM) on its way to L2, and its tensor maps
       for (int tok = kCtaTokens * rank; tok < min(kCtaTokens * static_cast<int>(rank + 1), nx.ntok); ++tok)
@@ -1456,8 +1463,8 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
 // the helper warp: looks special blocks' V over, stores finished tiles
 // ---------------------------------------------------------------------------------------
 template <bool kFp8>
-__device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnArgs& a, int g,
-                           uint32_t rank) {
+__device__ void run_helper(Smem& S, const CUtensorMap* q_map, const CUtensorMap* out_map,
+                           const ChunkAttnArgs& a, int g, uint32_t rank) {
   using C = Cfg<kFp8>;
   volatile int* abort = &S.abort_flag;
   const int lane = threadIdx.x & 31;
@@ -1469,6 +1476,7 @@ __device__ void run_helper(Smem& S, const CUtensorMap* out_map, const ChunkAttnA
   Item it;
   while (cur.next(it)) {
     const int n = it.blk1 - it.blk0;
+    if (!kFp8 && item == 0 && leader) load_q(S, q_map, a, it, rank);
     uint32_t bad = 0;
     for (int blk = max(it.blk0, it.special()); blk < it.blk1; ++blk) {
       const int t = blk - it.blk0;
@@ -1583,7 +1591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) run_mma<kFp8>(S, a, g, tmem);
   } else if (warp == kHelperWarp) {
-    run_helper<kFp8>(S, &out_map, a, g, rank);
+    run_helper<kFp8>(S, &q_map, &out_map, a, g, rank);
   } else {
     run_softmax<kFp8>(S, a, g, rank, tmem);
   }
@@ -1615,15 +1623,21 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(Chunk
   pdl_launch_dependents();
   pdl_wait();
   const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int2 info = __ldcg(&a.info[g]);
-  const int parts = info.y >> 3, ntok = info.y & 7;
   const int row0 = blockIdx.y * kCombineRows, row = row0 + lane;
   const int dim0 = blockIdx.z * kCombineDims;
-  if (row0 >= ntok * kHeads) return;
   // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
   auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
-  float M = -INFINITY;
-  for (int i = 0; i < parts; ++i) {
+  // (the first two parts' maxima with the information that they are there: a pair beyond the
+  // last is not looked at)
+  const int2 info = __ldcg(&a.info[g]);
+  const int g1 = min(g + 1, static_cast<int>(gridDim.x) - 1);
+  float M = __ldcg(slot_m(a.partials, 2 * g + 1) + row);
+  const float m1 = __ldcg(slot_m(a.partials, 2 * g1) + row);
+  const int parts = info.y >> 3, ntok = info.y & 7;
+  if (row0 >= ntok * kHeads) return;
+  M = max3(M, m1, m1);  // (there are two parts or more)
+#pragma unroll 4
+  for (int i = 2; i < parts; ++i) {
     const float m = __ldcg(slot_m(a.partials, slot(i)) + row);
     M = max3(M, m, m);
   }
