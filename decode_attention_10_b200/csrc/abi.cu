@@ -320,7 +320,7 @@ using namespace mfa;
 
 extern "C" {
 
-int32_t mfa_version(void) { return 100; }
+int32_t mfa_version(void) { return 200; }
 
 const char* mfa_status_str(int32_t status) {
   switch (status) {
@@ -376,7 +376,7 @@ mfa_status mfa_kv_table_init(void* table, size_t table_bytes, int32_t batch, int
     host[b].k = k_ptrs[b];
     host[b].v = v_ptrs[b];
     host[b].capacity = capacity[b];
-    host[b].chunk_maps = chunk;
+    host[b].chunk_maps = chunk ? chunk_maps_offset(batch, b) : 0;
   }
   return store_table(table, host, maps, static_cast<cudaStream_t>(stream));
 }
@@ -424,12 +424,12 @@ mfa_status mfa_kv_table_init_paged(void* table, size_t table_bytes, int32_t batc
   proto.v = v_pool;
   proto.page_size = page_size;
   proto.num_pages = num_pages;
-  proto.chunk_maps = chunk;
   std::vector<KvSeq> host(batch, proto);
   const std::vector<KvChunkMaps> maps(chunk ? batch : 0, proto_maps);
   for (int b = 0; b < batch; ++b) {
     host[b].capacity = pages_per_seq[b] * page_size;
     host[b].pages = page_table + (size_t)b * max_pages;
+    host[b].chunk_maps = chunk ? chunk_maps_offset(batch, b) : 0;
   }
   return store_table(table, host, maps, static_cast<cudaStream_t>(stream));
 }

@@ -38,7 +38,7 @@
 // ends inside a tile leaves (m, l, O) partials in one of the pair's two slots, merged in a
 // fixed order by chunk_combine_kernel. Where there are fewer tiles than pairs, each tile is
 // instead cut evenly among pairs of its own if that is about as short: half as many partials,
-// and no pair has two items (32 sequences of 4096 and 4 tokens: 47.5 -> SHARED us).
+// and no pair has two items (32 sequences of 4096 and 4 tokens: 46.2 -> 44.7 us).
 //
 // Blocks that hold keys some token of the tile does not see are "special": at most the last
 // two of a tile. Their scores are masked by selection, so nothing a hidden key holds reaches a
@@ -684,7 +684,6 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   volatile int* abort = &S.abort_flag;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
-  const KvChunkMaps* maps = reinterpret_cast<const KvChunkMaps*>(a.kv + a.batch);
   const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
   const int page_shift = kPaged ? 31 - __clz(a.page_size) : 0;
   uint32_t chunk = 0, issued = 0, specials = 0;
@@ -694,11 +693,11 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   Item it, nx;
   bool has = cur.next(it);
   if (!kPaged && has && leader) {
-    prefetch_tensormap(&maps[it.b].k);
-    prefetch_tensormap(&maps[it.b].v);
+    prefetch_tensormap(&chunk_maps(a.kv[it.b])->k);
+    prefetch_tensormap(&chunk_maps(a.kv[it.b])->v);
   }
   while (has) {
-    const KvChunkMaps* map = kPaged ? maps : maps + it.b;  // (one pool)
+    const KvChunkMaps* map = chunk_maps(a.kv[kPaged ? 0 : it.b]);  // (paged: one pool)
     if constexpr (!kFp8) {
       if (item > 0) {  // (the first item's Q is loaded by the helper warp meanwhile)
         mbar_wait(&S.q_empty, (item - 1) & 1, abort);
@@ -790,8 +789,8 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
       for (int tok = kCtaTokens * rank; tok < min(kCtaTokens * static_cast<int>(rank + 1), nx.ntok); ++tok)
         for (int c = 0; c < 4; ++c) tma_prefetch_2d(q_map, 64 * c, (nx.row0 + tok) * kHeads);
       if constexpr (!kPaged) {
-        prefetch_tensormap(&maps[nx.b].k);
-        prefetch_tensormap(&maps[nx.b].v);
+        prefetch_tensormap(&chunk_maps(a.kv[nx.b])->k);
+        prefetch_tensormap(&chunk_maps(a.kv[nx.b])->v);
       }
     }
     for (int blk = it.blk0; blk < it.blk1; ++blk) {
@@ -1044,15 +1043,16 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
     const int r = r0 + 2 * i;
     const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
                            v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-    float mx = 0.f;
+    // magnitudes of bf16 values compare as whole numbers (NaN above infinity)
+    uint32_t mx = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+    for (int k = 1; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // 128 <= mx 2^-e < 256; e >= -100 keeps 2^-e finite; a row with an infinity (its scores are
-    // NaN anyhow) and one of zeros take 0. (A subnormal mx counts as 2^-127.)
-    const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-    const int e = mx > 0.f && ex < 255 ? max(ex - 127 - 7, -100) : 0;
+    for (int o = 8; o > 0; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const int ex = static_cast<int>(max(mx & 0xFFFFu, mx >> 16) >> 7);
+    // 128 <= largest 2^-e < 256; e >= -100 keeps 2^-e finite; a row with an infinity or NaN (its
+    // scores are NaN anyhow) and one of zeros or subnormals take 0
+    const int e = ex > 0 && ex < 255 ? max(ex - 127 - 7, -100) : 0;
     const float sc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     if (part == 0) S.q_exp[r] = e;
     uint32_t hi[4], lo[4];
@@ -1570,7 +1570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&out_map);
     if (kPaged) {  // (the table is the host's; no kernel writes it)
-      const KvChunkMaps* maps = reinterpret_cast<const KvChunkMaps*>(a.kv + a.batch);
+      const KvChunkMaps* maps = chunk_maps(a.kv[0]);
       prefetch_tensormap(&maps->k);
       prefetch_tensormap(&maps->v);
     }

@@ -52,7 +52,7 @@ struct alignas(128) KvSeq {
   int32_t page_size;      // 0: contiguous
   const int32_t* pages;   // paged: this sequence's row of the page table (device)
   int32_t num_pages;      // paged: pages in each pool
-  int32_t chunk_maps;     // 1: the table goes on with a KvChunkMaps per sequence
+  int32_t chunk_maps;     // bytes from this entry to its KvChunkMaps, 0: the table has none
   int32_t reserved[22];
 };
 static_assert(sizeof(KvSeq) == 384, "KvSeq layout");
@@ -64,6 +64,15 @@ struct alignas(128) KvChunkMaps {
   CUtensorMap v;
 };
 constexpr int kChunkBoxRows = 64;
+
+// (Found from the entry itself, so that a description of fewer sequences than the table was
+// made for finds them too.)
+__device__ __forceinline__ const KvChunkMaps* chunk_maps(const KvSeq& s) {
+  return reinterpret_cast<const KvChunkMaps*>(reinterpret_cast<const uint8_t*>(&s) + s.chunk_maps);
+}
+inline int32_t chunk_maps_offset(int batch, int b) {
+  return static_cast<int32_t>(sizeof(KvSeq) * (batch - b) + sizeof(KvChunkMaps) * b);
+}
 
 // The element row, in its K or V buffer (or pool), of cache row `row` of sequence s: the
 // sequence's own row, or for a paged cache row % page_size of page pages[row / page_size].

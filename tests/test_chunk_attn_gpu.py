@@ -260,6 +260,21 @@ def test_table_without_chunk_maps_is_refused():
     assert mfa.get_error(ws) == 1 and (out == 5.0).all()
 
 
+@KV
+@LAYOUT
+def test_fewer_sequences_than_the_table(fp8, page):
+    # a description of a table's first sequences
+    from decode_attention_10_b200 import mfa
+    b = Batch([3, 9, 1, 5], [60, 200, 70, 1], fp8, page, seed=23)
+    cache = b.cache()
+    cache.desc.batch = cache.batch = 2
+    ws = mfa.ChunkWorkspace(2)
+    out = mfa.chunk_attn(b.q[:12], cache, b.q_start[:3], b.seq_lens[:2], ws=ws)
+    ref, tol = b.reference()
+    assert mfa.get_error(ws) == 0
+    assert ((out.double() - ref[:12]).abs() <= tol[:12]).all()
+
+
 def test_page_outside_the_pool_reads_as_zeros():
     # as in mfa_decode_attn: such a page's keys and values are zeros
     b = Batch([3], [300], False, 64, seed=19)
