@@ -1043,16 +1043,15 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
     const int r = r0 + 2 * i;
     const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
                            v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-    // magnitudes of bf16 values compare as whole numbers (NaN above infinity)
-    uint32_t mx = w[0] & 0x7FFF7FFFu;
+    float mx = 0.f;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const int ex = static_cast<int>(max(mx & 0xFFFFu, mx >> 16) >> 7);
-    // 128 <= largest 2^-e < 256; e >= -100 keeps 2^-e finite; a row with an infinity or NaN (its
-    // scores are NaN anyhow) and one of zeros or subnormals take 0
-    const int e = ex > 0 && ex < 255 ? max(ex - 127 - 7, -100) : 0;
+    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 128 <= mx 2^-e < 256; e >= -100 keeps 2^-e finite; a row with an infinity (its scores are
+    // NaN anyhow) and one of zeros take 0. (A subnormal mx counts as 2^-127.)
+    const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
+    const int e = mx > 0.f && ex < 255 ? max(ex - 127 - 7, -100) : 0;
     const float sc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     if (part == 0) S.q_exp[r] = e;
     uint32_t hi[4], lo[4];
