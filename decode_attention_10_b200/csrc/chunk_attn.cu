@@ -48,6 +48,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "mfa_internal.cuh"
 #include "sm100.cuh"
 
@@ -433,13 +435,16 @@ struct Cursor {
 __device__ __forceinline__ bool share_tiles(Plan& P, int tiles, int t0, int mine, int lo, int hi, int b0,
                                             int b1, int batch, int g, int pairs) {
   const int lane = threadIdx.x & 31;
-  const int total = P.cost[batch], most = (total + pairs - 1) / pairs + kPartCost;
   lo = __reduce_min_sync(0xffffffffu, mine > 0 ? lo : 1 << 30);
   hi = __reduce_max_sync(0xffffffffu, mine > 0 ? hi : 0);
+  // a block takes 1.1 us and merging a part 0.5 us, so parts shorter than this do not pay (one
+  // token over 8000 positions: 47 us as 63 parts, 22 us as 11)
+  const int least = max(1, static_cast<int>(sqrtf(0.45f * hi) + 0.5f));
+  const int total = P.cost[batch], most = max(least, (total + pairs - 1) / pairs + kPartCost);
   int tile, part, k, blk = hi;
   if (lo == hi) {  // all alike (decoding, or one tile): no search
     const int split = min(pairs / tiles, hi);
-    const int M = (hi + split - 1) / split;
+    const int M = max(least, (hi + split - 1) / split);
     if (M > most) return false;
     k = (hi + M - 1) / M;
     tile = g / k;
@@ -456,7 +461,7 @@ __device__ __forceinline__ bool share_tiles(Plan& P, int tiles, int t0, int mine
     int c[kPer], ks[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) c[j] = kPer * lane + j < tiles ? P.tile_blk[kPer * lane + j] : 0;
-    int M = (total - tiles * kTileCost + pairs - 1) / pairs, sum = 0;
+    int M = max(least, (total - tiles * kTileCost + pairs - 1) / pairs), sum = 0;
     for (;; ++M) {
       if (M > most) return false;
       const float r = 1.f / M;
@@ -1626,39 +1631,53 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(Chunk
   const int dim0 = blockIdx.z * kCombineDims;
   // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
   auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
-  // (the first two parts' maxima with the information that they are there: a pair beyond the
-  // last is not looked at)
   const int2 info = __ldcg(&a.info[g]);
-  const int g1 = min(g + 1, static_cast<int>(gridDim.x) - 1);
-  float M = __ldcg(slot_m(a.partials, 2 * g + 1) + row);
-  const float m1 = __ldcg(slot_m(a.partials, 2 * g1) + row);
   const int parts = info.y >> 3, ntok = info.y & 7;
   if (row0 >= ntok * kHeads) return;
-  M = max3(M, m1, m1);  // (there are two parts or more)
-#pragma unroll 4
-  for (int i = 2; i < parts; ++i) {
-    const float m = __ldcg(slot_m(a.partials, slot(i)) + row);
-    M = max3(M, m, m);
-  }
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[16] = {};
-#pragma unroll 2
-  for (int i = 0; i < parts; ++i) {
-    const float* acc = slot_acc(a.partials, slot(i)) + ((dim0 / 4 + 4 * warp) * kChunkRows + row) * 4;
-    float4 x[4];
+  // two or four parts' loads at a time, none of which waits for a maximum: the sums so far are
+  // scaled down when it rises
+  float M = -INFINITY, L = 0.f, o[16] = {};
+  auto merge = [&](int i0, auto ahead) {
+    constexpr int kAhead = decltype(ahead)::value;
+    float m[kAhead], l[kAhead];
+    float4 x[kAhead][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      x[k] = __ldcg(reinterpret_cast<const float4*>(acc + k * kChunkRows * 4));
-    const float w = ex2(__ldcg(slot_m(a.partials, slot(i)) + row) - base);
-    L = fmaf(w, __ldcg(slot_l(a.partials, slot(i)) + row), L);
+    for (int j = 0; j < kAhead; ++j) {
+      const bool there = i0 + j < parts;
+      const int sl = slot(i0 + j);
+      const float* acc = slot_acc(a.partials, sl) + ((dim0 / 4 + 4 * warp) * kChunkRows + row) * 4;
+      m[j] = there ? __ldcg(slot_m(a.partials, sl) + row) : -INFINITY;
+      l[j] = there ? __ldcg(slot_l(a.partials, sl) + row) : 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[4 * k] = fmaf(w, x[k].x, o[4 * k]);
-      o[4 * k + 1] = fmaf(w, x[k].y, o[4 * k + 1]);
-      o[4 * k + 2] = fmaf(w, x[k].z, o[4 * k + 2]);
-      o[4 * k + 3] = fmaf(w, x[k].w, o[4 * k + 3]);
+      for (int k = 0; k < 4; ++k)
+        x[j][k] = there ? __ldcg(reinterpret_cast<const float4*>(acc + k * kChunkRows * 4))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  }
+    float mn = M;
+#pragma unroll
+    for (int j = 0; j < kAhead; j += 2) mn = max3(mn, m[j], m[j + 1]);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float down = ex2(M - base);  // (0 at first)
+    M = mn;
+    L *= down;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) o[d] *= down;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const float w = ex2(m[j] - base);
+      L = fmaf(w, l[j], L);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[4 * k] = fmaf(w, x[j][k].x, o[4 * k]);
+        o[4 * k + 1] = fmaf(w, x[j][k].y, o[4 * k + 1]);
+        o[4 * k + 2] = fmaf(w, x[j][k].z, o[4 * k + 2]);
+        o[4 * k + 3] = fmaf(w, x[j][k].w, o[4 * k + 3]);
+      }
+    }
+  };
+  merge(0, std::integral_constant<int, 2>());
+#pragma unroll 1
+  for (int i = 2; i < parts; i += 4) merge(i, std::integral_constant<int, 4>());
   const float inv = (a.kv_dtype == MFA_KV_FP8_E4M3 ? a.v_scale : 1.f) / L;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
