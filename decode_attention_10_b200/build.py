@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libmfa.so")
 BINDING = os.path.join(HERE, "mfa_torch.so")
 SOURCES = ["abi.cu", "query_path.cu", "gemm_tc.cu", "attention_tc.cu", "out_proj.cu", "noalloc.cu",
            "selftest.cu", "split_plan.cu", "rope_append.cu", "chunk_attn.cu"]
-HEADERS = ["mfa_internal.cuh", "attn_plan.cuh", "sm100.cuh"]
+HEADERS = ["mfa_internal.cuh", "attn_plan.cuh", "sm100.cuh", "chunk.cuh"]
 
 
 def nvcc_path() -> str:

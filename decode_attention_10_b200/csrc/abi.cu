@@ -8,6 +8,7 @@
 #include <new>
 #include <vector>
 
+#include "chunk.cuh"
 #include "mfa_internal.cuh"
 
 // A captured decode step (include/mfa.h): the instantiated graph and the device it was
@@ -376,7 +377,7 @@ mfa_status mfa_kv_table_init(void* table, size_t table_bytes, int32_t batch, int
     host[b].k = k_ptrs[b];
     host[b].v = v_ptrs[b];
     host[b].capacity = capacity[b];
-    host[b].chunk_maps = chunk ? chunk_maps_offset(batch, b) : 0;
+    if (chunk) set_chunk_maps(host[b], batch, b);
   }
   return store_table(table, host, maps, static_cast<cudaStream_t>(stream));
 }
@@ -429,7 +430,7 @@ mfa_status mfa_kv_table_init_paged(void* table, size_t table_bytes, int32_t batc
   for (int b = 0; b < batch; ++b) {
     host[b].capacity = pages_per_seq[b] * page_size;
     host[b].pages = page_table + (size_t)b * max_pages;
-    host[b].chunk_maps = chunk ? chunk_maps_offset(batch, b) : 0;
+    if (chunk) set_chunk_maps(host[b], batch, b);
   }
   return store_table(table, host, maps, static_cast<cudaStream_t>(stream));
 }

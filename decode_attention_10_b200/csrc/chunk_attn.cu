@@ -50,7 +50,7 @@
 
 #include <type_traits>
 
-#include "mfa_internal.cuh"
+#include "chunk.cuh"
 #include "sm100.cuh"
 
 namespace mfa {
@@ -532,7 +532,7 @@ __device__ __forceinline__ uint32_t read_sequence(const ChunkAttnArgs& a, int b,
   s0 = a.q_start[b], s1 = a.q_start[b + 1], len = a.seq_lens[b];
   const KvSeq& kv = a.kv[b];
   cost = 0;
-  if (kv.chunk_maps == 0 || kv.page_size != a.page_size || s0 < 0 || s1 < s0 || s1 > a.n_rows)
+  if (!has_chunk_maps(kv) || kv.page_size != a.page_size || s0 < 0 || s1 < s0 || s1 > a.n_rows)
     return kErrLayout;
   if (s1 == s0) return 0;
   const uint32_t bits = len > kv.capacity ? kErrCapacity : len < s1 - s0 ? kErrEmpty : 0u;

@@ -22,7 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include "mfa_internal.cuh"
+#include "chunk.cuh"
 #include "sm100.cuh"
 
 namespace mfa {
