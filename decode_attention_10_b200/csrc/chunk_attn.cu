@@ -165,9 +165,10 @@ __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
   return r;
 }
 
-// Arrive on a barrier of either CTA. The plain form orders what tensor memory needs (with
-// tcgen05.fence) and nothing that the other CTA reads from shared memory; the release form also
-// does that, and waits for a fence of ~1000 cycles, so it is for special blocks only.
+// Arrive on a barrier of either CTA. The plain form is for what the tensor cores read: tensor
+// memory (with tcgen05.fence) and the arriving CTA's own shared memory (with fence.proxy.async).
+// The release form also orders what threads of the other CTA read, and waits ~1000 cycles for
+// that: for flags only.
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -1221,9 +1222,8 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
     split_q(S, a, x, rank, swarp, lane);
     fence_proxy_async_smem();
     named_bar_sync(7, 32 * kSoftmaxWarps);  // q_exp (and every warp's part is in place)
-    const float f = mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[row]) << 23);
-    if (st == 0) remote_arrive_release(q_bar);
-    return f;
+    if (st == 0) remote_arrive(q_bar);
+    return mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[row]) << 23);
   };
   if constexpr (kFp8) {
     if (has) mul = next_q(it);
