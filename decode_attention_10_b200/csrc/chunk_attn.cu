@@ -74,6 +74,7 @@ constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
 constexpr int kTileCost = 3;  // a tile's fixed cost, in blocks (Q, first softmax, epilogue)
 constexpr int kPartCost = 2;  // what a second part in a pair costs over a tile's start, in blocks
 constexpr int kMaxShared = 128;  // (pairs of SMs, at most)
+static_assert(2 * kMaxShared >= kMaxAttnGrid, "every pair");
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
@@ -438,9 +439,10 @@ __device__ __forceinline__ bool share_tiles(Plan& P, int tiles, int t0, int mine
   const int lane = threadIdx.x & 31;
   lo = __reduce_min_sync(0xffffffffu, mine > 0 ? lo : 1 << 30);
   hi = __reduce_max_sync(0xffffffffu, mine > 0 ? hi : 0);
-  // a block takes 1.1 us and merging a part 0.5 us, so parts shorter than this do not pay (one
-  // token over 8000 positions: 47 us as 63 parts, 22 us as 11)
-  const int least = max(1, static_cast<int>(sqrtf(0.45f * hi) + 0.5f));
+  // a block takes 1.1 us and merging a part 0.1 to 0.5 us, so parts shorter than this do not pay
+  // (one token over 8000 positions: 16.6 us as 25 parts of five blocks; four blocks a part 17.7,
+  // eight 17.7)
+  const int least = max(1, static_cast<int>(sqrtf(0.2f * hi) + 0.5f));
   const int total = P.cost[batch], most = max(least, (total + pairs - 1) / pairs + kPartCost);
   int tile, part, k, blk = hi;
   if (lo == hi) {  // all alike (decoding, or one tile): no search
@@ -1617,23 +1619,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------------------
 // merge of the tiles that several pairs share, in a fixed order. A block takes 32 rows and 64
-// dimensions of one tile: lane = row, warp = 16 of the dimensions.
+// dimensions of one tile: lane = row, warp = 16 of the dimensions and, where there may be many
+// parts (few tokens, long contexts), one of kGroups shares of them.
 // ---------------------------------------------------------------------------------------
-constexpr int kCombineWarps = 4;
-constexpr int kCombineRows = 32, kCombineDims = 16 * kCombineWarps;
+constexpr int kCombineRows = 32, kCombineDims = 64;
+constexpr int kDimWarps = kCombineDims / 16;
+// With this few tokens a tile may have dozens of parts, and four shares of them at a time pay; with
+// more there are a few parts a tile, and the blocks of four times the threads cost more than they
+// save. Measured, four shares against one: one token over 60,000 positions 31.4 and 60.4 us, 12
+// tokens over 30,000 33.5 and 43.6; 16 sequences of one token over 1500 22.8 and 18.3, 12 over 4000
+// 25.4 and 23.4.
+constexpr int kFewRows = 12;
 
-__global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(ChunkAttnArgs a) {
+template <int kGroups>
+__global__ void __launch_bounds__(32 * kDimWarps * kGroups) chunk_combine_kernel(ChunkAttnArgs a) {
+  constexpr int kThreadsC = 32 * kDimWarps * kGroups;
   __shared__ __align__(16) uint4 tile[kCombineRows][kCombineDims / 8 + 1];
+  __shared__ float share[kGroups > 1 ? kGroups - 1 : 1][18][32 * kDimWarps];
   pdl_launch_dependents();
   pdl_wait();
-  const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) % kDimWarps, group = (threadIdx.x >> 5) / kDimWarps;
   const int row0 = blockIdx.y * kCombineRows, row = row0 + lane;
   const int dim0 = blockIdx.z * kCombineDims;
-  // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
-  auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
-  const int2 info = __ldcg(&a.info[g]);
+  // the pair in which the tile begins, the blockIdx.x-th of those with a split tile (every warp
+  // looks for it)
+  int g = blockIdx.x;
+  int2 info = make_int2(0, 0);
+  if constexpr (kGroups == 1) {
+    info = __ldcg(&a.info[g]);
+  } else {
+    g = -1;
+    int2 all[kMaxShared / 32];
+#pragma unroll
+    for (int j = 0; j < kMaxShared / 32; ++j) {
+      const int i = 32 * j + lane;
+      all[j] = i < a.pairs ? __ldcg(&a.info[i]) : make_int2(0, 0);
+    }
+    int left = blockIdx.x;
+#pragma unroll
+    for (int j = 0; j < kMaxShared / 32; ++j) {
+      const uint32_t some = __ballot_sync(0xffffffffu, all[j].y != 0);
+      const int n = __popc(some);
+      if (g < 0 && left < n) {
+        const int l = __fns(some, 0, left + 1);
+        info.x = __shfl_sync(0xffffffffu, all[j].x, l);
+        info.y = __shfl_sync(0xffffffffu, all[j].y, l);
+        g = 32 * j + l;
+      }
+      left -= n;
+    }
+  }
   const int parts = info.y >> 3, ntok = info.y & 7;
   if (row0 >= ntok * kHeads) return;
+  // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
+  auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
   // two or four parts' loads at a time, none of which waits for a maximum: the sums so far are
   // scaled down when it rises
   float M = -INFINITY, L = 0.f, o[16] = {};
@@ -1675,18 +1715,48 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(Chunk
       }
     }
   };
-  merge(0, std::integral_constant<int, 2>());
+  if constexpr (kGroups == 1) {
+    merge(0, std::integral_constant<int, 2>());
 #pragma unroll 1
-  for (int i = 2; i < parts; i += 4) merge(i, std::integral_constant<int, 4>());
+    for (int i = 2; i < parts; i += 4) merge(i, std::integral_constant<int, 4>());
+  } else {
+#pragma unroll 1
+    for (int i = 4 * group; i < parts; i += 4 * kGroups) merge(i, std::integral_constant<int, 4>());
+    const int at = 32 * warp + lane;
+    if (group > 0) {
+      float (*mine)[32 * kDimWarps] = share[group - 1];
+      mine[0][at] = M;
+      mine[1][at] = L;
+#pragma unroll
+      for (int d = 0; d < 16; ++d) mine[2 + d][at] = o[d];
+    }
+    __syncthreads();
+    if (group == 0) {
+      float mn = M;
+#pragma unroll
+      for (int j = 0; j < kGroups - 1; ++j) mn = max3(mn, share[j][0][at], share[j][0][at]);
+      const float base = mn == -INFINITY ? 0.f : mn, down = ex2(M - base);
+      L *= down;
+#pragma unroll
+      for (int d = 0; d < 16; ++d) o[d] *= down;
+#pragma unroll
+      for (int j = 0; j < kGroups - 1; ++j) {
+        const float w = ex2(share[j][0][at] - base);
+        L = fmaf(w, share[j][1][at], L);
+#pragma unroll
+        for (int d = 0; d < 16; ++d) o[d] = fmaf(w, share[j][2 + d][at], o[d]);
+      }
+    }
+  }
   const float inv = (a.kv_dtype == MFA_KV_FP8_E4M3 ? a.v_scale : 1.f) / L;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < 2 && group == 0; ++k)
     tile[lane][2 * warp + k] = make_uint4(
         pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
         pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
   __syncthreads();
   // whole 128-byte lines of the rows
-  for (int i = threadIdx.x; i < kCombineRows * (kCombineDims / 8); i += 32 * kCombineWarps) {
+  for (int i = threadIdx.x; i < kCombineRows * (kCombineDims / 8); i += kThreadsC) {
     const int r = i / (kCombineDims / 8), piece = i % (kCombineDims / 8);
     *reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(info.x) * kHeads + row0 + r) * kHeadDim + dim0 +
                               8 * piece) = tile[r][piece];
@@ -1736,9 +1806,14 @@ cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const CUtensorMap& out_m
   const cudaError_t e =
       launch_pdl(kernel, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, q_map, out_map, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_combine_kernel,
-                    dim3(a.pairs, kChunkRows / kCombineRows, kHeadDim / kCombineDims),
-                    dim3(32 * kCombineWarps), 0, s, a);
+  // split tiles, and rows of one, that there can be
+  const int tiles = a.n_rows < a.pairs ? a.n_rows : a.pairs;
+  const int rows = (a.n_rows < kTokens ? a.n_rows : kTokens) * kHeads;
+  const bool few = a.n_rows <= kFewRows;
+  const dim3 grid(few ? tiles : a.pairs, rows / kCombineRows, kHeadDim / kCombineDims);
+  if (few)
+    return launch_pdl(chunk_combine_kernel<4>, grid, dim3(32 * kDimWarps * 4), 0, s, a);
+  return launch_pdl(chunk_combine_kernel<1>, grid, dim3(32 * kDimWarps), 0, s, a);
 }
 
 }  // namespace mfa
