@@ -58,7 +58,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
            os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
            sysconfig.get_paths()["include"]]
     libs = os.path.join(base, "lib")
-    tmp = BINDING + ".tmp"
+    tmp = f"{BINDING}.{os.getpid()}.tmp"  # (two ranks may build at once)
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{i}" for i in inc], src, "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch",

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -45,6 +46,12 @@ bool device_sms(int* sms) {
 bool encode_rows(CUtensorMap* m, void* base, int rows, int dtype, int box_rows) {
   const int elem = dtype == MFA_KV_FP8_E4M3 ? 1 : 2;
   return encode_2d(m, base, (uint64_t)rows, kHeadDim, elem, 128 / elem, box_rows);
+}
+
+// whether two arrays of `bytes` bytes overlap
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < bytes;
 }
 
 // a device array of int32
@@ -578,6 +585,8 @@ mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, const voi
   if (!valid_ints(q_start) || !valid_ints(seq_lens)) return MFA_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_out == nullptr)) return MFA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(q_out)) return MFA_ERR_INVALID_ARG;
+  if (q != q_out && overlap(q, q_out, (size_t)n_rows * kHeads * kHeadDim * 2))
+    return MFA_ERR_INVALID_ARG;
   RopeAppendArgs a{};
   if (rope != nullptr) {
     if (rope->table == nullptr || !aligned16(rope->table) || rope->max_pos < 1)
@@ -624,10 +633,13 @@ mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* 
                           void* ws, size_t ws_bytes, void* stream) {
   mfa_status st = check_kv(kv);
   if (st != MFA_OK) return st;
-  if (n_rows < 1 || n_rows > MFA_MAX_ROWS || !(scale > 0.f)) return MFA_ERR_INVALID_ARG;
+  if (n_rows < 1 || n_rows > MFA_MAX_ROWS) return MFA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || std::isinf(scale)) return MFA_ERR_INVALID_ARG;
   const void* ptrs[] = {q, out};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MFA_ERR_INVALID_ARG;
+  // (tiles are written while other pairs of SMs still read theirs)
+  if (overlap(q, out, (size_t)n_rows * kHeads * kHeadDim * 2)) return MFA_ERR_INVALID_ARG;
   if (!valid_ints(q_start) || !valid_ints(seq_lens)) return MFA_ERR_INVALID_ARG;
   WsLayout L;
   st = check_ws(ws, ws_bytes, kv->batch, &L);

@@ -4,7 +4,7 @@
 // the tensors' attributes from Python took longer (5 us) than the launch itself (2.7 us).
 //
 // Each function returns the mfa_status of the call, or -1 - i if its i-th tensor argument is
-// not what the call takes (the caller then finds the words).
+// not what the call takes, or kOtherDevice (the caller then finds the words).
 #include <Python.h>
 
 #include <c10/cuda/CUDAFunctions.h>
@@ -39,6 +39,17 @@ bool ready(Py_ssize_t n_args, Py_ssize_t takes) {
   PyErr_SetString(PyExc_TypeError, "wrong number of arguments, or no library bound");
   return false;
 }
+
+// The current device; -1 without one (no tensor of a device is there then).
+int current_device() {
+  c10::DeviceIndex dev = 0;
+  return c10::cuda::GetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+// What the cache, the workspace and the rotation's table have their memory on (`o`, a device's
+// index) is not the current device.
+constexpr long kOtherDevice = -100;
+bool elsewhere(PyObject* o, int dev) { return PyLong_AsLong(o) != dev; }
 
 // A tensor argument; false if it is none.
 bool tensor(PyObject* o, const Tensor** t) {
@@ -76,12 +87,11 @@ void* stream_of(PyObject* o, int dev) {
 PyObject* refused(int i) { return PyLong_FromLong(-1 - i); }
 
 // rope_append(q|None, k, v, cache, batch, q_start, seq_lens, rope, axes, positions|None,
-//             q_out|None, ws, ws_bytes, stream|None)
+//             q_out|None, ws, ws_bytes, stream|None, device)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  if (!ready(n_args, 14)) return nullptr;
+  if (!ready(n_args, 15)) return nullptr;
   try {
-    c10::DeviceIndex dev = 0;
-    if (c10::cuda::GetDevice(&dev) != cudaSuccess) dev = -1;  // (no tensor is there then)
+    const int dev = current_device();
     const Tensor *q = nullptr, *k, *v, *q_start, *seq_lens, *pos = nullptr, *q_out = nullptr;
     if (!tensor(a[1], &k) || k->dim() != 2) return refused(0);
     const int64_t n = k->size(0), batch = PyLong_AsLongLong(a[4]), axes = PyLong_AsLongLong(a[8]);
@@ -107,6 +117,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     void* ws = PyLong_AsVoidPtr(a[11]);
     const size_t ws_bytes = PyLong_AsSize_t(a[12]);
     void* stream = stream_of(a[13], dev);
+    if (elsewhere(a[14], dev) && !PyErr_Occurred()) return PyLong_FromLong(kOtherDevice);
     if (PyErr_Occurred()) return nullptr;
     return PyLong_FromLong(f_rope_append(
         q ? q->data_ptr() : nullptr, k->data_ptr(), static_cast<int32_t>(k_ld), v->data_ptr(),
@@ -120,12 +131,11 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   }
 }
 
-// chunk_attn(q, cache, batch, q_start, seq_lens, scale, out, ws, ws_bytes, stream|None)
+// chunk_attn(q, cache, batch, q_start, seq_lens, scale, out, ws, ws_bytes, stream|None, device)
 PyObject* chunk_attn(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  if (!ready(n_args, 10)) return nullptr;
+  if (!ready(n_args, 11)) return nullptr;
   try {
-    c10::DeviceIndex dev = 0;
-    if (c10::cuda::GetDevice(&dev) != cudaSuccess) dev = -1;  // (no tensor is there then)
+    const int dev = current_device();
     const Tensor *q, *q_start, *seq_lens, *out;
     if (!tensor(a[0], &q) || q->dim() != 3) return refused(0);
     const int64_t n = q->size(0), batch = PyLong_AsLongLong(a[2]);
@@ -138,6 +148,7 @@ PyObject* chunk_attn(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     void* ws = PyLong_AsVoidPtr(a[7]);
     const size_t ws_bytes = PyLong_AsSize_t(a[8]);
     void* stream = stream_of(a[9], dev);
+    if (elsewhere(a[10], dev) && !PyErr_Occurred()) return PyLong_FromLong(kOtherDevice);
     if (PyErr_Occurred()) return nullptr;
     return PyLong_FromLong(f_chunk_attn(
         q->data_ptr(), kv, static_cast<const int32_t*>(q_start->data_ptr()),

@@ -5,6 +5,7 @@ torch tensors into pointers, picks the current CUDA stream, and raises on error 
 There is no fallback: if the library is missing, the first call raises.
 """
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -197,7 +198,7 @@ class KVCache:
                "mfa_kv_table_init")
         self.desc = KvCacheDesc(self.batch, self.dtype, self.k_scale, self.v_scale,
                                 self.table.data_ptr(), 0)
-        self.addr = ctypes.addressof(self.desc)
+        self.addr, self.device_index = ctypes.addressof(self.desc), self.table.get_device()
 
 
 class PagedKVCache:
@@ -243,7 +244,7 @@ class PagedKVCache:
                "mfa_kv_table_init_paged")
         self.desc = KvCacheDesc(self.batch, self.dtype, self.k_scale, self.v_scale,
                                 self.table.data_ptr(), self.page_size)
-        self.addr = ctypes.addressof(self.desc)
+        self.addr, self.device_index = ctypes.addressof(self.desc), self.table.get_device()
 
 
 class BlockFP8Weight:
@@ -276,7 +277,7 @@ class Workspace:
             raise ValueError(f"batch {batch} out of range (or no CUDA device)")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8,
                                device=device if device is not None else "cuda")
-        self.addr = self.buf.data_ptr()
+        self.addr, self.device_index = self.buf.data_ptr(), self.buf.get_device()
         _check(lib.mfa_workspace_init(self.addr, self.nbytes, _stream(stream)),
                "mfa_workspace_init")
 
@@ -321,7 +322,7 @@ class Rope:
         self.n_axes = max(axes) + 1
         self.desc = RopeDesc(_ptr(table), int(table.shape[0]), self.rot_dim, int(interleaved),
                              self.n_axes, (ctypes.c_uint8 * (HEAD_DIM // 2))(*axes))
-        self.addr = ctypes.addressof(self.desc)
+        self.addr, self.device_index = ctypes.addressof(self.desc), table.get_device()
 
 
 def get_error(ws: Workspace, stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -383,10 +384,13 @@ def decode_layer(x, w_qdown, gamma, w_qup, w_k, w_v, cache: KVCache, seq_lens,
 
 
 def _refuse(status: int, where: str, *tensors):
-    """Raise for what a call of mfa_torch returned: the library's status, or -1 - i for the
-    i-th of the tensors (name, tensor, dtype, shape, dense)."""
+    """Raise for what a call of mfa_torch returned: the library's status, -1 - i for the i-th of
+    the tensors (name, tensor, dtype, shape, dense), or -100 for another device."""
     if status > 0:
         raise MfaError(status, where)
+    if status == -100:
+        raise ValueError(f"{where}: the cache and the workspace are not on the current device, "
+                         f"cuda:{torch.cuda.current_device()}")
     what, t, dtype, shape, dense = tensors[-1 - status]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a tensor")
@@ -401,6 +405,18 @@ def _refuse(status: int, where: str, *tensors):
     if dense:
         raise ValueError(f"{what}: expected a contiguous tensor")
     raise ValueError(f"{what}: its rows must be dense and less than 2^31 elements apart")
+
+
+def _device(cache, ws, rope=None) -> int:
+    dev = cache.device_index
+    if ws.device_index != dev or (rope is not None and rope.device_index != dev):
+        raise ValueError("the cache, the workspace and the rope's table must be on one device")
+    return dev
+
+
+def _made_on(stream: Optional[torch.cuda.Stream]):
+    """What a call allocates itself belongs to the stream that it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
@@ -418,13 +434,16 @@ def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
         if q_out is not None:
             raise ValueError("q_out without q")
     elif q_out is None:
-        q_out = torch.empty_like(q)
+        with _made_on(stream):
+            q_out = torch.empty_like(q)
     if ws is None:
-        ws = Workspace(batch, k.device)
+        with _made_on(stream):
+            ws = Workspace(batch, k.device)
     addr, axes = (0, 0) if rope is None else (rope.addr, rope.n_axes)
     st = _chunk.rope_append(q, k, v, cache.addr, batch, q_start, seq_lens, addr, axes, positions,
                             q_out, ws.addr, ws.nbytes,
-                            None if stream is None else stream.cuda_stream)
+                            None if stream is None else stream.cuda_stream,
+                            _device(cache, ws, rope))
     if st != 0:
         n = k.shape[0]
         row, heads = (n, HEAD_DIM), (n, N_HEADS, HEAD_DIM)
@@ -447,11 +466,14 @@ def chunk_attn(q, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
         load()
     batch = cache.batch
     if out is None:
-        out = torch.empty_like(q)
+        with _made_on(stream):
+            out = torch.empty_like(q)
     if ws is None:
-        ws = ChunkWorkspace(batch, q.device)
+        with _made_on(stream):
+            ws = ChunkWorkspace(batch, q.device)
     st = _chunk.chunk_attn(q, cache.addr, batch, q_start, seq_lens, scale, out, ws.addr,
-                           ws.nbytes, None if stream is None else stream.cuda_stream)
+                           ws.nbytes, None if stream is None else stream.cuda_stream,
+                           _device(cache, ws))
     if st != 0:
         heads = (q.shape[0], N_HEADS, HEAD_DIM)
         _refuse(st, "mfa_chunk_attn", ("q", q, torch.bfloat16, heads, True),

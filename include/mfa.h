@@ -308,7 +308,8 @@ typedef struct {
  *   q_out = bf16(R(p) q);  K row j <- bf16(R(p) k), V row j <- bf16(v), or for FP8 caches
  *   e4m3(R(p) k / k_scale) and e4m3(v / v_scale),  j the token's position in its sequence.
  * The rotation runs in float32 and is rounded once.
- *   q: device bf16 [n_rows, 64, 256] or NULL (append only); q_out: as q, or q itself.
+ *   q: device bf16 [n_rows, 64, 256] or NULL (append only); q_out: as q, not overlapping it,
+ *   or q itself.
  *   k, v: device bf16, row t at element t * k_ld (v_ld); k_ld and v_ld are multiples of 8,
  *   at least 256, so that k and v may be halves of one projection's output.
  *   rope: host pointer, NULL = no rotation (then q must be NULL: nothing would happen to it).
@@ -335,7 +336,7 @@ MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, c
  * included, and do not reach its result. For FP8 caches the cached codes are used exactly, q
  * as in mfa_decode_attn with one power-of-two scale per token and head, and the softmax weights
  * as e4m3 pairs within 2^-8 of their value or 2^-14 of the row's largest weight.
- * q: device bf16 [n_rows, 64, 256]; out: device bf16 [n_rows, 64, 256]; scale > 0.
+ * q, out: device bf16 [n_rows, 64, 256], not overlapping; scale: positive and finite.
  * kv: a table of mfa_chunk_table_bytes(kv->batch) bytes or more.
  * ws: device workspace of mfa_chunk_workspace_bytes(kv->batch) bytes (initialized once).
  * A sequence with new tokens and seq_lens[b] > capacity[b] (MFA_ERR_CAPACITY) or seq_lens[b] <

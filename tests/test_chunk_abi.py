@@ -35,7 +35,7 @@ def test_table_sizes(lib):
 
 
 def test_chunk_attention_refusals(lib):
-    def call(q=FAKE, c=None, starts=FAKE, lens=FAKE, n=5, scale=0.0625, out=FAKE, ws=FAKE,
+    def call(q=FAKE, c=None, starts=FAKE, lens=FAKE, n=5, scale=0.0625, out=P(1 << 30), ws=FAKE,
              size=BIG):
         return lib.mfa_chunk_attn(q, c if c is not None else kv(), starts, lens, n, scale, out,
                                   ws, size, None)
@@ -43,7 +43,8 @@ def test_chunk_attention_refusals(lib):
     for bad in (dict(q=None), dict(q=P(4104)), dict(out=None), dict(out=P(4100)),
                 dict(starts=None), dict(starts=P(4098)), dict(lens=None), dict(lens=P(4097)),
                 dict(n=0), dict(n=-1), dict(n=mfa.MAX_ROWS + 1), dict(scale=0.0),
-                dict(scale=-1.0), dict(scale=math.nan), dict(ws=None), dict(ws=P(4096 + 16)),
+                dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(out=FAKE),
+                dict(out=P(4096 + 5 * 32768 - 16)), dict(q=P((1 << 30) + 16)), dict(ws=None), dict(ws=P(4096 + 16)),
                 dict(c=kv(batch=0)), dict(c=kv(batch=1025)), dict(c=kv(table=None)),
                 dict(c=kv(table=4096 + 64)), dict(c=kv(page=96)), dict(c=kv(page=32)),
                 dict(c=kv(dtype=1, k=0.0)), dict(c=kv(dtype=1, v=-1.0))):
@@ -64,7 +65,8 @@ def test_rope_append_refusals(lib):
 
     for bad in (dict(k=None), dict(k=P(4100)), dict(v=None), dict(v=P(4104)), dict(k_ld=255),
                 dict(k_ld=260), dict(v_ld=128), dict(v_ld=257), dict(q=None), dict(out=None),
-                dict(q=P(4104)), dict(out=P(4104)), dict(starts=None), dict(lens=None),
+                dict(q=P(4104)), dict(out=P(4104)), dict(out=P(4112)), dict(q=P(5 * 32768)),
+                dict(starts=None), dict(lens=None),
                 dict(starts=P(4098)), dict(n=0), dict(n=mfa.MAX_ROWS + 1), dict(r=None),
                 dict(r=rope(table=None)), dict(r=rope(table=4100)), dict(r=rope(max_pos=0)),
                 dict(r=rope(rot=0)), dict(r=rope(rot=8)), dict(r=rope(rot=24)),
@@ -77,11 +79,15 @@ def test_rope_append_refusals(lib):
     assert call(c=kv(dtype=9)) == 2
 
 
+def far_rope():
+    return type("R", (), {"addr": 4096, "n_axes": 1, "device_index": 1})()
+
+
 def test_binding_refusals(lib):
     # (a workspace and a cache that no call gets as far as using)
-    ws = type("W", (), {"addr": 4096, "nbytes": BIG})()
+    ws = type("W", (), {"addr": 4096, "nbytes": BIG, "device_index": 0})()
     desc = mfa.KvCacheDesc(2, 0, 1.0, 1.0, 4096, 0)
-    cache = type("C", (), {"batch": 2, "addr": ctypes.addressof(desc)})()
+    cache = type("C", (), {"batch": 2, "addr": ctypes.addressof(desc), "device_index": 0})()
     starts, lens = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     q = torch.zeros(4, 64, 256, dtype=torch.bfloat16)
     kv = torch.zeros(4, 512, dtype=torch.bfloat16)
@@ -109,7 +115,7 @@ def test_binding_refusals(lib):
             mfa._refuse(-1, "", args)
     with pytest.raises(mfa.MfaError, match="MFA_ERR_WORKSPACE"):
         mfa._refuse(4, "x")
-    for name, n in (("rope_append", 14), ("chunk_attn", 10), ("bind", 2)):
+    for name, n in (("rope_append", 15), ("chunk_attn", 11), ("bind", 2)):
         with pytest.raises(TypeError):
             getattr(mfa._chunk, name)(*[0] * (n - 1))
     with pytest.raises(ValueError, match="rot_dim"):
@@ -119,6 +125,12 @@ def test_binding_refusals(lib):
     for axes in ([0] * 15, [0] * 15 + [4], [-1] * 16):
         with pytest.raises(ValueError, match="pair_axis"):
             mfa.Rope(torch.zeros(5, 32), axes)
+    # memory on several devices
+    far = type("W", (), {"addr": 4096, "nbytes": BIG, "device_index": 1})()
+    with pytest.raises(ValueError, match="one device"):
+        mfa.chunk_attn(q, cache, starts, lens, out=q, ws=far)
+    with pytest.raises(ValueError, match="one device"):
+        mfa.rope_append(q, k, v, cache, starts, lens, rope=far_rope(), ws=ws)
     # what the binding passes on: a table of the wrong place
     with pytest.raises(ValueError, match="CUDA"):
         mfa.Rope(torch.zeros(5, 32))

@@ -332,3 +332,48 @@ def test_two_calls_on_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+def test_own_results_and_workspace_on_a_given_stream():
+    # what a call allocates itself is not handed out again before the given stream is done
+    from decode_attention_10_b200 import mfa
+    b = Batch([300, 2], [6000, 9000], False, 64, seed=23)
+    cache, want, s = b.cache(), run(b), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(6):
+        out = mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, stream=s)
+        junk = [torch.full((1 << 23,), float("nan"), device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del junk
+
+
+@KV
+@pytest.mark.parametrize("new,cached", [
+    ([1], [60000]), ([12], [9000]), ([13], [9000]), ([2, 0, 3, 7], [30000, 5, 257, 8000]),
+    ([1] * 12, [3000 + 700 * i for i in range(12)]),
+    ([1] * 13, [3000 + 700 * i for i in range(13)]),
+])
+def test_few_tokens_over_long_contexts(fp8, new, cached):
+    # many parts a tile: merged by several shares of them up to 12 tokens, by one beyond
+    b = Batch(new, cached, fp8, 256, seed=24)
+    check(run(b), b)
+
+
+def test_memory_of_another_device_is_refused():
+    from decode_attention_10_b200 import mfa
+    b = Batch([3], [40], False, 64, seed=25)
+    cache, ws = b.cache(), mfa.ChunkWorkspace(1)
+    cache.device_index = ws.device_index = torch.cuda.current_device() + 1
+    with pytest.raises(ValueError, match="not on the current device"):
+        mfa.chunk_attn(b.q, cache, b.q_start, b.seq_lens, ws=ws)
+    k = torch.zeros(3, DIM, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="not on the current device"):
+        mfa.rope_append(None, k, k, cache, b.q_start, b.seq_lens, ws=ws)
+
+
+def test_results_over_the_queries_are_refused():
+    from decode_attention_10_b200 import mfa
+    b = Batch([5], [40], False, 64, seed=26)
+    with pytest.raises(mfa.MfaError, match="INVALID_ARG"):
+        mfa.chunk_attn(b.q, b.cache(), b.q_start, b.seq_lens, out=b.q)
