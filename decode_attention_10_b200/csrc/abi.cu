@@ -634,7 +634,7 @@ mfa_status mfa_chunk_attn(const void* q, const mfa_kv_cache* kv, const int32_t* 
   mfa_status st = check_kv(kv);
   if (st != MFA_OK) return st;
   if (n_rows < 1 || n_rows > MFA_MAX_ROWS) return MFA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || std::isinf(scale)) return MFA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isnormal(scale)) return MFA_ERR_INVALID_ARG;
   const void* ptrs[] = {q, out};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MFA_ERR_INVALID_ARG;

@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "chunk.cuh"
@@ -1225,7 +1226,8 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
     fence_proxy_async_smem();
     named_bar_sync(7, 32 * kSoftmaxWarps);  // q_exp (and every warp's part is in place)
     if (st == 0) remote_arrive(q_bar);
-    return mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[row]) << 23);
+    // (not 0, by which a hidden key's -infinity would become NaN: scores this small are all alike)
+    return fmaxf(mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[row]) << 23), FLT_MIN);
   };
   if constexpr (kFp8) {
     if (has) mul = next_q(it);

@@ -336,7 +336,7 @@ MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, c
  * included, and do not reach its result. For FP8 caches the cached codes are used exactly, q
  * as in mfa_decode_attn with one power-of-two scale per token and head, and the softmax weights
  * as e4m3 pairs within 2^-8 of their value or 2^-14 of the row's largest weight.
- * q, out: device bf16 [n_rows, 64, 256], not overlapping; scale: positive and finite.
+ * q, out: device bf16 [n_rows, 64, 256], not overlapping; scale: positive, a normal float.
  * kv: a table of mfa_chunk_table_bytes(kv->batch) bytes or more.
  * ws: device workspace of mfa_chunk_workspace_bytes(kv->batch) bytes (initialized once).
  * A sequence with new tokens and seq_lens[b] > capacity[b] (MFA_ERR_CAPACITY) or seq_lens[b] <

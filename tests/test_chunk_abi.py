@@ -43,8 +43,10 @@ def test_chunk_attention_refusals(lib):
     for bad in (dict(q=None), dict(q=P(4104)), dict(out=None), dict(out=P(4100)),
                 dict(starts=None), dict(starts=P(4098)), dict(lens=None), dict(lens=P(4097)),
                 dict(n=0), dict(n=-1), dict(n=mfa.MAX_ROWS + 1), dict(scale=0.0),
-                dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(out=FAKE),
-                dict(out=P(4096 + 5 * 32768 - 16)), dict(q=P((1 << 30) + 16)), dict(ws=None), dict(ws=P(4096 + 16)),
+                dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=1e-40),
+                dict(out=FAKE),
+                dict(out=P(4096 + 5 * 32768 - 16)), dict(q=P((1 << 30) + 16)), dict(ws=None),
+                dict(ws=P(4096 + 16)),
                 dict(c=kv(batch=0)), dict(c=kv(batch=1025)), dict(c=kv(table=None)),
                 dict(c=kv(table=4096 + 64)), dict(c=kv(page=96)), dict(c=kv(page=32)),
                 dict(c=kv(dtype=1, k=0.0)), dict(c=kv(dtype=1, v=-1.0))):

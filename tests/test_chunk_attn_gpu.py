@@ -183,6 +183,14 @@ def test_scale_is_an_argument(fp8):
 
 
 @KV
+@pytest.mark.parametrize("scale,q_scale", [(1e-37, 1e-5), (1e-20, 1e-30), (3e-6, 1.0), (50.0, 1e-4)])
+def test_tiny_and_large_scales(fp8, scale, q_scale):
+    # down to factors of the scores that float32 cannot hold
+    b = Batch([6], [250], fp8, 64, seed=27, q_scale=q_scale)
+    check(run(b, scale=scale), b, scale=scale)
+
+
+@KV
 def test_agrees_with_the_decode_attention(fp8):
     # one new token a sequence is mfa_decode_attn
     from decode_attention_10_b200 import mfa
