@@ -1587,7 +1587,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   cluster_arrive();  // this CTA's barriers are set up
-  pdl_launch_dependents();
   pdl_wait();
   build_plan(S, a, g, static_cast<int>(gridDim.x) / 2, blockIdx.x == 0);
   cluster_wait();  // and the other's
@@ -1606,6 +1605,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // (not earlier: see the merge)
+  pdl_launch_dependents();
   if (threadIdx.x == 0 && S.abort_flag) atomicOr(a.err, kErrTimeout);
   // the last commit of the products reaches both CTAs: neither may be gone by then
   if (warp == 1 && rank != 0) mbar_wait_drain(&S.mma_done, 0);
@@ -1620,78 +1621,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// merge of the tiles that several pairs share, in a fixed order. A block takes 32 rows and 64
-// dimensions of one tile: lane = row, warp = 16 of the dimensions and, where there may be many
-// parts (few tokens, long contexts), one of kGroups shares of them.
+// merge of the tiles that several pairs share, in a fixed order. A block takes 32 rows (half a
+// token) of one tile: lane = row, four warps of kDims dimensions each. Bound by the latency of its
+// loads and by how evenly its blocks lie: their launch is triggered at the end of a pair's work, so
+// that they do not gather on the SMs that have none (12 sequences of one token over 4000 positions:
+// 24.4 us when triggered at the start, 20.7 so).
 // ---------------------------------------------------------------------------------------
-constexpr int kCombineRows = 32, kCombineDims = 64;
-constexpr int kDimWarps = kCombineDims / 16;
-// With this few tokens a tile may have dozens of parts, and four shares of them at a time pay; with
-// more there are a few parts a tile, and the blocks of four times the threads cost more than they
-// save. Measured, four shares against one: one token over 60,000 positions 31.4 and 60.4 us, 12
-// tokens over 30,000 33.5 and 43.6; 16 sequences of one token over 1500 22.8 and 18.3, 12 over 4000
-// 25.4 and 23.4.
-constexpr int kFewRows = 12;
+constexpr int kCombineRows = 32, kCombineWarps = 4;
+static_assert(kHeads == 2 * kCombineRows, "a token is two blocks of rows");
+// By a whole warp: the `token`-th token of all split tiles, as its tile's info, the pair in which
+// that begins, and the token of the tile; zeros if there are fewer. (Each lane looks at kPer pairs
+// in a row.)
+__device__ __forceinline__ int4 find_token(const ChunkAttnArgs& a, int token) {
+  constexpr int kPer = kMaxShared / 32;
+  const int lane = threadIdx.x & 31;
+  int2 info[kPer];
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int g = kPer * lane + j;
+    info[j] = g < a.pairs ? __ldcg(&a.info[g]) : make_int2(0, 0);
+    mine += info[j].y & 7;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  int4 r = make_int4(0, 0, 0, 0);
+  int left = token - (upto - mine);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int n = info[j].y & 7;
+    if (left >= 0 && left < n) r = make_int4(info[j].x, info[j].y, kPer * lane + j, left);
+    left -= n;
+  }
+  const uint32_t who = __ballot_sync(0xffffffffu, r.y != 0);
+  const int from = who != 0 ? __ffs(who) - 1 : 0;
+  r.x = __shfl_sync(0xffffffffu, r.x, from);
+  r.y = __shfl_sync(0xffffffffu, r.y, from);
+  r.z = __shfl_sync(0xffffffffu, r.z, from);
+  r.w = __shfl_sync(0xffffffffu, r.w, from);
+  return r;
+}
 
-template <int kGroups>
-__global__ void __launch_bounds__(32 * kDimWarps * kGroups) chunk_combine_kernel(ChunkAttnArgs a) {
-  constexpr int kThreadsC = 32 * kDimWarps * kGroups;
-  __shared__ __align__(16) uint4 tile[kCombineRows][kCombineDims / 8 + 1];
-  __shared__ float share[kGroups > 1 ? kGroups - 1 : 1][18][32 * kDimWarps];
+// Up to this many tiles, which may have a dozen parts and more each, 8 dimensions a thread and 16
+// parts' loads at a time; above it 16 dimensions and four parts. Measured, the first and the second:
+// one token over 60,000 positions 29.8 and 36.8 us, 12 over 30,000 29.9 and 33.3; 12 sequences of
+// one token over 200 12.9 and 11.6, 16 over 1500 17.6 and 16.5.
+constexpr int kFewTiles = 6;
+// Up to this many tokens, blocks for the tokens that there are, which look for their tile; above it
+// blocks for every pair and row, most of which end at once. The first and the second: 24 tokens over
+// 3000 positions 18.0 and 24.2 us, 64 sequences of one over 200 14.3 and 15.4; 25 of 4 over 500 17.8
+// and 16.5, 100 tokens over 900 19.0 and 18.1 (and a prompt of 1111 tokens 63 and 56: every block
+// reads the pairs' few lines).
+constexpr int kFewTokens = 64;
+
+template <int kDims, int kAtOnce, bool kSearch>
+__global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(ChunkAttnArgs a) {
+  constexpr int kBlockDims = kDims * kCombineWarps;
+  __shared__ __align__(16) uint4 tile[kCombineRows][kBlockDims / 8 + 1];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int warp = (threadIdx.x >> 5) % kDimWarps, group = (threadIdx.x >> 5) / kDimWarps;
-  const int row0 = blockIdx.y * kCombineRows, row = row0 + lane;
-  const int dim0 = blockIdx.z * kCombineDims;
-  // the pair in which the tile begins, the blockIdx.x-th of those with a split tile (every warp
-  // looks for it)
-  int g = blockIdx.x;
-  int2 info = make_int2(0, 0);
-  if constexpr (kGroups == 1) {
-    info = __ldcg(&a.info[g]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int dim0 = blockIdx.y * kBlockDims;
+  // the tile, the pair g in which it begins, and its row
+  int2 info;
+  int g, row0;
+  if constexpr (kSearch) {
+    // Block x takes half x % 2 of the (x / 2)-th token of all split tiles.
+    __shared__ int4 found;
+    if (warp == 0) found = find_token(a, blockIdx.x / 2);
+    __syncthreads();
+    info = make_int2(found.x, found.y);
+    g = found.z;
+    row0 = found.w * kHeads + (blockIdx.x & 1) * kCombineRows;
+    if (info.y == 0) return;
   } else {
-    g = -1;
-    int2 all[kMaxShared / 32];
-#pragma unroll
-    for (int j = 0; j < kMaxShared / 32; ++j) {
-      const int i = 32 * j + lane;
-      all[j] = i < a.pairs ? __ldcg(&a.info[i]) : make_int2(0, 0);
-    }
-    int left = blockIdx.x;
-#pragma unroll
-    for (int j = 0; j < kMaxShared / 32; ++j) {
-      const uint32_t some = __ballot_sync(0xffffffffu, all[j].y != 0);
-      const int n = __popc(some);
-      if (g < 0 && left < n) {
-        const int l = __fns(some, 0, left + 1);
-        info.x = __shfl_sync(0xffffffffu, all[j].x, l);
-        info.y = __shfl_sync(0xffffffffu, all[j].y, l);
-        g = 32 * j + l;
-      }
-      left -= n;
-    }
+    g = blockIdx.x;
+    info = __ldcg(&a.info[g]);
+    row0 = blockIdx.z * kCombineRows;
+    if (row0 >= (info.y & 7) * kHeads) return;
   }
-  const int parts = info.y >> 3, ntok = info.y & 7;
-  if (row0 >= ntok * kHeads) return;
+  const int parts = info.y >> 3, row = row0 + lane;
   // part i of the tile lies in the first slot of pair g + i, part 0 in g's second
   auto slot = [&](int i) { return i == 0 ? 2 * g + 1 : 2 * (g + i); };
-  // two or four parts' loads at a time, none of which waits for a maximum: the sums so far are
+  // two, then kAtOnce parts' loads at a time, none of which waits for a maximum: the sums so far are
   // scaled down when it rises
-  float M = -INFINITY, L = 0.f, o[16] = {};
+  float M = -INFINITY, L = 0.f, o[kDims] = {};
   auto merge = [&](int i0, auto ahead) {
     constexpr int kAhead = decltype(ahead)::value;
     float m[kAhead], l[kAhead];
-    float4 x[kAhead][4];
+    float4 x[kAhead][kDims / 4];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const bool there = i0 + j < parts;
       const int sl = slot(i0 + j);
-      const float* acc = slot_acc(a.partials, sl) + ((dim0 / 4 + 4 * warp) * kChunkRows + row) * 4;
+      const float* acc = slot_acc(a.partials, sl) + ((dim0 + kDims * warp) * kChunkRows + row * 4);
       m[j] = there ? __ldcg(slot_m(a.partials, sl) + row) : -INFINITY;
       l[j] = there ? __ldcg(slot_l(a.partials, sl) + row) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < kDims / 4; ++k)
         x[j][k] = there ? __ldcg(reinterpret_cast<const float4*>(acc + k * kChunkRows * 4))
                         : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -1703,13 +1734,13 @@ __global__ void __launch_bounds__(32 * kDimWarps * kGroups) chunk_combine_kernel
     M = mn;
     L *= down;
 #pragma unroll
-    for (int d = 0; d < 16; ++d) o[d] *= down;
+    for (int d = 0; d < kDims; ++d) o[d] *= down;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const float w = ex2(m[j] - base);
       L = fmaf(w, l[j], L);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kDims / 4; ++k) {
         o[4 * k] = fmaf(w, x[j][k].x, o[4 * k]);
         o[4 * k + 1] = fmaf(w, x[j][k].y, o[4 * k + 1]);
         o[4 * k + 2] = fmaf(w, x[j][k].z, o[4 * k + 2]);
@@ -1717,49 +1748,23 @@ __global__ void __launch_bounds__(32 * kDimWarps * kGroups) chunk_combine_kernel
       }
     }
   };
-  if constexpr (kGroups == 1) {
-    merge(0, std::integral_constant<int, 2>());
+  merge(0, std::integral_constant<int, 2>());
+  int i = 2;
+  constexpr int kRest = kAtOnce > 8 ? kAtOnce / 2 : 0;  // (what the last, smaller step takes)
 #pragma unroll 1
-    for (int i = 2; i < parts; i += 4) merge(i, std::integral_constant<int, 4>());
-  } else {
-#pragma unroll 1
-    for (int i = 4 * group; i < parts; i += 4 * kGroups) merge(i, std::integral_constant<int, 4>());
-    const int at = 32 * warp + lane;
-    if (group > 0) {
-      float (*mine)[32 * kDimWarps] = share[group - 1];
-      mine[0][at] = M;
-      mine[1][at] = L;
-#pragma unroll
-      for (int d = 0; d < 16; ++d) mine[2 + d][at] = o[d];
-    }
-    __syncthreads();
-    if (group == 0) {
-      float mn = M;
-#pragma unroll
-      for (int j = 0; j < kGroups - 1; ++j) mn = max3(mn, share[j][0][at], share[j][0][at]);
-      const float base = mn == -INFINITY ? 0.f : mn, down = ex2(M - base);
-      L *= down;
-#pragma unroll
-      for (int d = 0; d < 16; ++d) o[d] *= down;
-#pragma unroll
-      for (int j = 0; j < kGroups - 1; ++j) {
-        const float w = ex2(share[j][0][at] - base);
-        L = fmaf(w, share[j][1][at], L);
-#pragma unroll
-        for (int d = 0; d < 16; ++d) o[d] = fmaf(w, share[j][2 + d][at], o[d]);
-      }
-    }
-  }
+  for (; i + kRest < parts; i += kAtOnce) merge(i, std::integral_constant<int, kAtOnce>());
+  if constexpr (kRest > 0)
+    if (i < parts) merge(i, std::integral_constant<int, kRest>());
   const float inv = (a.kv_dtype == MFA_KV_FP8_E4M3 ? a.v_scale : 1.f) / L;
 #pragma unroll
-  for (int k = 0; k < 2 && group == 0; ++k)
-    tile[lane][2 * warp + k] = make_uint4(
+  for (int k = 0; k < kDims / 8; ++k)
+    tile[lane][kDims / 8 * warp + k] = make_uint4(
         pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
         pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
   __syncthreads();
-  // whole 128-byte lines of the rows
-  for (int i = threadIdx.x; i < kCombineRows * (kCombineDims / 8); i += kThreadsC) {
-    const int r = i / (kCombineDims / 8), piece = i % (kCombineDims / 8);
+  // whole sectors of the rows
+  for (int p = threadIdx.x; p < kCombineRows * (kBlockDims / 8); p += 32 * kCombineWarps) {
+    const int r = p / (kBlockDims / 8), piece = p % (kBlockDims / 8);
     *reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(info.x) * kHeads + row0 + r) * kHeadDim + dim0 +
                               8 * piece) = tile[r][piece];
   }
@@ -1808,14 +1813,15 @@ cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const CUtensorMap& out_m
   const cudaError_t e =
       launch_pdl(kernel, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, q_map, out_map, a);
   if (e != cudaSuccess) return e;
-  // split tiles, and rows of one, that there can be
-  const int tiles = a.n_rows < a.pairs ? a.n_rows : a.pairs;
-  const int rows = (a.n_rows < kTokens ? a.n_rows : kTokens) * kHeads;
-  const bool few = a.n_rows <= kFewRows;
-  const dim3 grid(few ? tiles : a.pairs, rows / kCombineRows, kHeadDim / kCombineDims);
-  if (few)
-    return launch_pdl(chunk_combine_kernel<4>, grid, dim3(32 * kDimWarps * 4), 0, s, a);
-  return launch_pdl(chunk_combine_kernel<1>, grid, dim3(32 * kDimWarps), 0, s, a);
+  const dim3 block(32 * kCombineWarps);
+  const auto dims = [](int n) { return kHeadDim / (n * kCombineWarps); };
+  if (a.n_rows > kFewTokens)
+    return launch_pdl(chunk_combine_kernel<16, 4, false>, dim3(a.pairs, dims(16), kChunkRows / kCombineRows),
+                      block, 0, s, a);
+  const int tiles = a.n_rows < a.batch ? a.n_rows : (a.n_rows + (kTokens - 1) * a.batch) / kTokens;  // at most
+  if (tiles <= kFewTiles)
+    return launch_pdl(chunk_combine_kernel<8, 16, true>, dim3(2 * a.n_rows, dims(8)), block, 0, s, a);
+  return launch_pdl(chunk_combine_kernel<16, 4, true>, dim3(2 * a.n_rows, dims(16)), block, 0, s, a);
 }
 
 }  // namespace mfa
