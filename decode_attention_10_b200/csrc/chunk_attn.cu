@@ -441,8 +441,7 @@ __device__ __forceinline__ bool share_tiles(Plan& P, int tiles, int t0, int mine
   lo = __reduce_min_sync(0xffffffffu, mine > 0 ? lo : 1 << 30);
   hi = __reduce_max_sync(0xffffffffu, mine > 0 ? hi : 0);
   // a block takes 1.1 us and merging a part 0.1 to 0.5 us, so parts shorter than this do not pay
-  // (one token over 8000 positions: 16.6 us as 25 parts of five blocks; four blocks a part 17.7,
-  // eight 17.7)
+  // (one token over 60,000 positions: 29.1 us in parts of 10 blocks, 31.4 of 7, 30.6 of 13)
   const int least = max(1, static_cast<int>(sqrtf(0.2f * hi) + 0.5f));
   const int total = P.cost[batch], most = max(least, (total + pairs - 1) / pairs + kPartCost);
   int tile, part, k, blk = hi;
@@ -1668,8 +1667,8 @@ __device__ __forceinline__ int4 find_token(const ChunkAttnArgs& a, int token) {
 
 // Up to this many tiles, which may have a dozen parts and more each, 8 dimensions a thread and 16
 // parts' loads at a time; above it 16 dimensions and four parts. Measured, the first and the second:
-// one token over 60,000 positions 29.8 and 36.8 us, 12 over 30,000 29.9 and 33.3; 12 sequences of
-// one token over 200 12.9 and 11.6, 16 over 1500 17.6 and 16.5.
+// one token over 60,000 positions 29.1 and 42.6 us, 12 over 30,000 29.3 and 36.3; 12 sequences of
+// one token over 200 11.9 and 11.3, 64 over 1500 28.0 and 26.8.
 constexpr int kFewTiles = 6;
 // Up to this many tokens, blocks for the tokens that there are, which look for their tile; above it
 // blocks for every pair and row, most of which end at once. The first and the second: 24 tokens over
@@ -1759,8 +1758,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(Chunk
 #pragma unroll
   for (int k = 0; k < kDims / 8; ++k)
     tile[lane][kDims / 8 * warp + k] = make_uint4(
-        pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-        pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+        pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+        pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+        pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
   __syncthreads();
   // whole sectors of the rows
   for (int p = threadIdx.x; p < kCombineRows * (kBlockDims / 8); p += 32 * kCombineWarps) {
@@ -1818,7 +1819,8 @@ cudaError_t launch_chunk_attn(const CUtensorMap& q_map, const CUtensorMap& out_m
   if (a.n_rows > kFewTokens)
     return launch_pdl(chunk_combine_kernel<16, 4, false>, dim3(a.pairs, dims(16), kChunkRows / kCombineRows),
                       block, 0, s, a);
-  const int tiles = a.n_rows < a.batch ? a.n_rows : (a.n_rows + (kTokens - 1) * a.batch) / kTokens;  // at most
+  // (at most)
+  const int tiles = a.n_rows < a.batch ? a.n_rows : (a.n_rows + (kTokens - 1) * a.batch) / kTokens;
   if (tiles <= kFewTiles)
     return launch_pdl(chunk_combine_kernel<8, 16, true>, dim3(2 * a.n_rows, dims(8)), block, 0, s, a);
   return launch_pdl(chunk_combine_kernel<16, 4, true>, dim3(2 * a.n_rows, dims(16)), block, 0, s, a);
