@@ -361,9 +361,11 @@ def test_own_results_and_workspace_on_a_given_stream():
     ([1], [60000]), ([12], [9000]), ([13], [9000]), ([2, 0, 3, 7], [30000, 5, 257, 8000]),
     ([1] * 12, [3000 + 700 * i for i in range(12)]),
     ([1] * 13, [3000 + 700 * i for i in range(13)]),
+    ([1] * 6, [9000] * 6), ([1] * 7, [9000] * 7), ([64], [3000]), ([65], [3000]),
+    ([25, 0, 39], [700, 64, 5000]), ([1] * 64, [900] * 64), ([1] * 65, [900] * 65),
 ])
 def test_few_tokens_over_long_contexts(fp8, new, cached):
-    # many parts a tile: merged by several shares of them up to 12 tokens, by one beyond
+    # many parts a tile, on both sides of the merge's choices (6 tiles, 64 tokens)
     b = Batch(new, cached, fp8, 256, seed=24)
     check(run(b), b)
 
