@@ -106,7 +106,11 @@ struct __align__(1024) Smem {
   uint8_t q[4 * kQChunkBytes];
   uint8_t ring[kSlots * kSlotBytes];
   Plan plan;
-  float xch[2][kRows];        // exchange between the two threads of a row
+  float xch[2][kRows];        // exchange between the two threads of a row: their maxima of a block
+  // their sums of an item. (Not in xch: a thread may come here before its partner has read the
+  // last block's maximum. Rows of missing tokens have neither, and no barrier: the next write
+  // here lies behind a barrier of a row that has, and so behind this item's reads.)
+  float sum[2][kRows];
   int32_t q_exp[kRows];       // FP8: exponent of each row's scale of Q
   uint64_t kv_full[kSlots];   // first CTA: both halves of a slot have landed (and are clean)
   uint64_t kv_empty[kSlots];
@@ -1372,10 +1376,12 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
 
     // ---- epilogue ----
     // what the next item needs goes first, while the last product runs
-    S.xch[half][row] = l;
+    if (real) S.sum[half][row] = l;
     const bool has_nx = cur.next(nx);
-    named_bar_sync(bar, 64);
-    l += S.xch[half ^ 1][row];
+    if (real) {
+      named_bar_sync(bar, 64);
+      l += S.sum[half ^ 1][row];
+    }
     const bool whole = it.whole();
     if constexpr (kFp8) {
       if (has_nx) next_mul = next_q(nx);
@@ -1457,7 +1463,6 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
       named_bar_sync(5 + half, 32 * kSoftmaxWarps / 2);
       if (st % 128 == 0) S.bad[item & 1][half] = 0;
     }
-    // (xch is written again only behind the pair's next barrier)
     it = nx;
     has = has_nx;
     mul = next_mul;
