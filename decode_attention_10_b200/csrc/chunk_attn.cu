@@ -111,7 +111,9 @@ struct __align__(1024) Smem {
   // last block's maximum. Rows of missing tokens have neither, and no barrier: the next write
   // here lies behind a barrier of a row that has, and so behind this item's reads.)
   float sum[2][kRows];
-  int32_t q_exp[kRows];       // FP8: exponent of each row's scale of Q
+  // FP8: exponent of each row's scale of Q, by the item's parity (warps write the next item's
+  // before all have read this one's; the barrier behind those orders the item after it)
+  int32_t q_exp[2][kRows];
   uint64_t kv_full[kSlots];   // first CTA: both halves of a slot have landed (and are clean)
   uint64_t kv_empty[kSlots];
   uint64_t q_full, q_empty;
@@ -1031,13 +1033,13 @@ __device__ __forceinline__ void load8(const void* base, long long at, float (&f)
 }
 
 // FP8: Q of an item, split into e4m3 high and low parts scaled by 2^-e with the row's largest
-// magnitude in [128, 256); e goes to S.q_exp. (bf16 times a power of two is exact in f16 down
+// magnitude in [128, 256); e goes to S.q_exp of the item's parity. (bf16 times a power of two is exact in f16 down
 // to 2^-24 of 256; smaller elements round there.) Each softmax warp takes 16 of the CTA's rows,
 // 16 lanes a row and 16 dimensions a lane, so that its loads cover whole lines (one row a
 // thread took 12000 cycles). The Q buffer must be free: every S of the previous item has
 // completed.
-__device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item& it, int rank,
-                                     int swarp, int lane) {
+__device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item& it, int parity,
+                                     int rank, int swarp, int lane) {
   constexpr int kRowsWarp = kRows / kSoftmaxWarps;
   const int part = lane % 16, r0 = swarp * kRowsWarp + lane / 16;
   const long long row0 = (static_cast<long long>(it.row0) + kCtaTokens * rank) * kHeads;
@@ -1065,7 +1067,7 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
     const int e = mx > 0.f && ex < 255 ? max(ex - 127 - 7, -100) : 0;
     const float sc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    if (part == 0) S.q_exp[r] = e;
+    if (part == 0) S.q_exp[parity][r] = e;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1224,16 +1226,16 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
   float mul = mul0;
   // FP8: the next item's Q into the buffer, once every S of this one is done, and its rows'
   // factor of the scores
-  auto next_q = [&](const Item& x) {
-    split_q(S, a, x, rank, swarp, lane);
+  auto next_q = [&](const Item& x, int parity) {
+    split_q(S, a, x, parity, rank, swarp, lane);
     fence_proxy_async_smem();
     named_bar_sync(7, 32 * kSoftmaxWarps);  // q_exp (and every warp's part is in place)
     if (st == 0) remote_arrive(q_bar);
     // (not 0, by which a hidden key's -infinity would become NaN: scores this small are all alike)
-    return fmaxf(mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[row]) << 23), FLT_MIN);
+    return fmaxf(mul0 * __uint_as_float(static_cast<uint32_t>(127 + S.q_exp[parity][row]) << 23), FLT_MIN);
   };
   if constexpr (kFp8) {
-    if (has) mul = next_q(it);
+    if (has) mul = next_q(it, 0);
   }
   while (has) {
     const int n = it.blk1 - it.blk0;
@@ -1384,7 +1386,7 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
     }
     const bool whole = it.whole();
     if constexpr (kFp8) {
-      if (has_nx) next_mul = next_q(nx);
+      if (has_nx) next_mul = next_q(nx, (item + 1) & 1);
     }
     if (whole) {
       mbar_wait(&S.stage_free, tiles & 1, abort);

@@ -3,8 +3,8 @@ of a pair of CTAs as coroutines that run in a random order, every barrier with i
 every buffer with what was last written to it. A wait is checked against the phase it means (the
 hardware sees its parity only), a read against the contents it means.
 
-The model takes the ring's sizes, and whether a row's sums have an array of their own, from the
-kernel's source."""
+The model takes the ring's sizes, whether a row's sums have an array of their own, and whether
+the exponents of two items' queries have, from the kernel's source."""
 
 import os
 import random
@@ -19,6 +19,7 @@ with open(os.path.join(CSRC, "chunk_attn.cu")) as _f:
 SLOTS, STAGE = (int(re.search(rf"constexpr int {name} = (\d+);", SOURCE).group(1))
                 for name in ("kSlots", "kStageSlots"))
 OWN_SUM = re.search(r"float sum\[2\]\[kRows\];", SOURCE) is not None
+TWO_EXPONENTS = re.search(r"int32_t q_exp\[2\]\[kRows\];", SOURCE) is not None
 QUADS = 2  # of the four: pairs of warps that share rows, in each CTA
 WARPS = [(quad, half) for quad in range(QUADS) for half in range(2)]
 
@@ -78,9 +79,10 @@ class Named:
 class Model:
     """items: (blocks, the special ones of them, whole tile, tokens of the tile) each."""
 
-    def __init__(self, seed, fp8, items, own_sum=OWN_SUM):
+    def __init__(self, seed, fp8, items, own_sum=OWN_SUM, two_exponents=TWO_EXPONENTS):
         self.rng = random.Random(seed)
         self.fp8, self.items, self.own_sum = fp8, items, own_sum
+        self.two_exponents = two_exponents
         self.ks = self.vs = 1 if fp8 else 2
         both, slots = range(2), range(SLOTS)
         warps = len(WARPS)
@@ -101,6 +103,7 @@ class Model:
         # what each buffer holds
         self.ring = [[None] * SLOTS for _ in both]
         self.q = [[None] * warps for _ in both]
+        self.q_exp = [[[None] * warps for _ in both] for _ in both]  # [CTA][item's parity][writer]
         self.xch, self.sum = ([[[None] * 2 for _ in range(QUADS)] for _ in both] for _ in both)
         self.bad = [[[0, 0], [0, 0]] for _ in both]  # [CTA][item's parity][V half]
         self.s_buf = [[[None] * warps for _ in both] for _ in both]  # [CTA][block's parity][warp]
@@ -232,11 +235,14 @@ class Model:
         sums = self.sum[r][quad] if self.own_sum else xch
 
         def next_q(k):
-            self.q[r][w] = k
+            exponents = self.q_exp[r][k & 1 if self.two_exponents else 0]
+            self.q[r][w] = exponents[w] = k
             yield self.all[r].sync()
             if w == 0:
                 self.q_full.arrive()
             yield None
+            rows = exponents[2 * quad:2 * quad + 2]  # (the rows of a pair were split by two warps)
+            expect(rows == [k, k], "exponent", k, rows)
 
         if self.fp8:
             yield from next_q(0)
@@ -379,3 +385,8 @@ def test_every_wait_and_every_read_means_what_it_gets(fp8):
 def test_the_model_sees_sums_that_overwrite_maxima():
     with pytest.raises(Fault, match="maximum"):
         schedules(250, False, own_sum=False)
+
+
+def test_the_model_sees_one_array_of_exponents():
+    with pytest.raises(Fault, match="exponent"):
+        schedules(250, True, two_exponents=False)
