@@ -128,7 +128,9 @@ struct __align__(1024) Smem {
   uint64_t stage_free;        // the ring slots for a tile's results are free
   uint64_t staged;            // this CTA's results of a tile are in them
   uint64_t mma_done;
-  uint32_t bad[2][2];         // [item parity][V half]: late rows held out of the product
+  // [item parity][V half]: late rows held out of the product (bad_flag). The item's number tells
+  // it from an older one, so nobody has to put it back to zero and wait for those who read it.
+  uint32_t bad[2][2];
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -1083,6 +1085,11 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
   }
 }
 
+__device__ __forceinline__ uint32_t bad_flag(int item, uint32_t rows) {
+  return (static_cast<uint32_t>(item + 1) << 3) | rows;
+}
+static_assert(kTokens - 1 <= 3, "a bit for each late row");
+
 // A special block's V half in this CTA's ring (its first slot's use `chunk`), by one warp: rows
 // of keys that no token of the tile sees are zeroed; rows that only its later tokens see (key
 // p0 + 1 + i, i < ntok - 1) are zeroed too if they hold an infinity or NaN, and their bits i
@@ -1396,8 +1403,11 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
     tc_fence_after();
     const bool ok = *abort == 0;
     const uint32_t o_addr = tmem + lane_addr + kTmemO + 128 * half;
-    // (volatile: written by the other CTA too)
-    const uint32_t bad = *static_cast<volatile uint32_t*>(&S.bad[item & 1][half]);
+    // (volatile: written by the other CTA too; the same in the whole warp, even where that happens
+    // meanwhile, after an abort)
+    const uint32_t flag = *static_cast<volatile uint32_t*>(&S.bad[item & 1][half]);
+    uint32_t bad = bad_flag(item, 0) ^ __shfl_sync(0xffffffffu, flag, 0);
+    if (bad >= 8) bad = 0;  // (an older item's)
     if (bad != 0) add_late<kFp8>(a, it, bad, tok, head, half, base - C::kPExp, o_addr);
     const int slot = 2 * g + (it.blk0 == 0 ? 1 : 0);
     if (whole) {
@@ -1460,11 +1470,6 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
       }
       if (it.blk0 == 0) info = make_int2(it.row0, it.parts * 8 + it.ntok);
     }
-    if (bad != 0) {
-      // the flag is spent: back to 0 once both halves' warps of this CTA have read it
-      named_bar_sync(5 + half, 32 * kSoftmaxWarps / 2);
-      if (st % 128 == 0) S.bad[item & 1][half] = 0;
-    }
     it = nx;
     has = has_nx;
     mul = next_mul;
@@ -1502,7 +1507,7 @@ __device__ void run_helper(Smem& S, const CUtensorMap* q_map, const CUtensorMap*
       if (__shfl_sync(0xffffffffu, *abort, 0) != 0) break;
       bad |= clean_v<kFp8>(S, it, blk, vc, lane);
       if (bad != 0 && lane < 2)  // for the epilogues of both CTAs
-        remote_store(map_to(&S.bad[item & 1][rank], lane), bad);
+        remote_store(map_to(&S.bad[item & 1][rank], lane), bad_flag(item, bad));
       fence_proxy_async_smem();
       __syncwarp();
       if (leader) {

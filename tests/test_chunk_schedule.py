@@ -4,7 +4,10 @@ every buffer with what was last written to it. A wait is checked against the pha
 hardware sees its parity only), a read against the contents it means.
 
 The model takes the ring's sizes, whether a row's sums have an array of their own, and whether
-the exponents of two items' queries have, from the kernel's source."""
+the exponents of two items' queries have, from the kernel's source.
+
+A wait that runs out aborts its CTA: none of its waits waits any more, nothing new is issued, and
+its producer has to wait for what is still in flight before the CTA may exit."""
 
 import os
 import random
@@ -20,6 +23,8 @@ SLOTS, STAGE = (int(re.search(rf"constexpr int {name} = (\d+);", SOURCE).group(1
                 for name in ("kSlots", "kStageSlots"))
 OWN_SUM = re.search(r"float sum\[2\]\[kRows\];", SOURCE) is not None
 TWO_EXPONENTS = re.search(r"int32_t q_exp\[2\]\[kRows\];", SOURCE) is not None
+NUMBERED = "bad_flag(" in SOURCE
+ISSUED = "v_issued" in SOURCE and "q_issued" in SOURCE
 QUADS = 2  # of the four: pairs of warps that share rows, in each CTA
 WARPS = [(quad, half) for quad in range(QUADS) for half in range(2)]
 
@@ -29,7 +34,7 @@ class Fault(AssertionError):
 
 
 def expect(ok, *what):
-    if not ok:
+    if not ok and (Bar.strict or what[0] == "hang"):
         raise Fault(what)
 
 
@@ -39,11 +44,15 @@ class Bar:
     def __init__(self, name, count):
         self.name, self.count, self.left, self.tx, self.phase = name, count, count, 0, 0
 
+    strict = True  # (not after an abort)
+
     def _turn(self):
         if self.left == 0 and self.tx == 0:
             self.phase, self.left = self.phase + 1, self.count
 
     def arrive(self, tx=0):
+        if self.left == 0 and not Bar.strict:
+            return
         expect(self.left > 0, "too many arrivals", self.name, self.phase)
         self.tx += tx
         self.left -= 1
@@ -57,8 +66,9 @@ class Bar:
         """A wait for `phase`, which is at most the current one when it returns."""
         def ready():
             seen = (self.phase & 1) != (phase & 1)
-            expect(seen == (self.phase > phase), "parity", self.name, phase, self.phase)
+            expect(seen == (self.phase > phase) or not Bar.strict, "parity", self.name, phase, self.phase)
             return seen
+        ready.bar = self
         return ready
 
 
@@ -79,10 +89,13 @@ class Named:
 class Model:
     """items: (blocks, the special ones of them, whole tile, tokens of the tile) each."""
 
-    def __init__(self, seed, fp8, items, own_sum=OWN_SUM, two_exponents=TWO_EXPONENTS):
+    def __init__(self, seed, fp8, items, own_sum=OWN_SUM, two_exponents=TWO_EXPONENTS,
+                 abort_at=None, numbered=NUMBERED, issued=ISSUED):
         self.rng = random.Random(seed)
         self.fp8, self.items, self.own_sum = fp8, items, own_sum
         self.two_exponents = two_exponents
+        self.abort_at, self.abort = abort_at, [False, False]
+        self.numbered, self.count_issued = numbered, issued
         self.ks = self.vs = 1 if fp8 else 2
         both, slots = range(2), range(SLOTS)
         warps = len(WARPS)
@@ -99,7 +112,7 @@ class Model:
         self.o_free = Bar("o_free", 2 * warps)
         self.pair = [[Named(2) for _ in range(QUADS)] for _ in both]
         self.all = [Named(warps) for _ in both]
-        self.late = [[Named(QUADS) for _ in both] for _ in both]
+        self.late = [[Named(QUADS) for _ in both] for _ in both]  # (planted)
         # what each buffer holds
         self.ring = [[None] * SLOTS for _ in both]
         self.q = [[None] * warps for _ in both]
@@ -119,13 +132,18 @@ class Model:
     def has_bad(self, half, k):
         return any(self.chance(.4, "bad", half, k, b) for b in sorted(self.items[k][1]))
 
+    def copy(self, r, bar, what=None):
+        """A copy of CTA r, which completes on `bar` in the phase that it has begun."""
+        self.copies.append((bar, what, r, bar.phase))
+
     def load_q(self, r):
         if r == 0:
             self.q_full.arrive(tx=2)
-        self.copies.append((self.q_full, None))
+        self.copy(r, self.q_full)
 
     def producer(self, r):
-        at = specials = 0
+        at = specials = issued = v_issued = 0
+        q_issued, abort = 1, self.abort
 
         def take():
             nonlocal at
@@ -137,28 +155,38 @@ class Model:
             return slot
 
         def load_k(k, b):
+            nonlocal issued
             for c in range(self.ks):
                 slot = yield from take()
+                if abort[r]:
+                    continue
                 self.kv_full[slot].arrive(tx=1)
-                self.copies.append((self.kv_full[slot], (r, slot, ("K", k, b, c))))
+                self.copy(r, self.kv_full[slot], (r, slot, ("K", k, b, c)))
+                issued = at
 
         def load_v(k, b):
-            nonlocal specials
+            nonlocal specials, issued, v_issued
             special, own = b in self.items[k][1], self.v_full[r][specials % SLOTS]
             for c in range(self.vs):
                 slot = yield from take()
+                if abort[r]:
+                    continue
                 if not special:
                     self.kv_full[slot].arrive(tx=1)
                 elif c == 0:
                     own.arrive(tx=self.vs)
-                self.copies.append((own if special else self.kv_full[slot],
-                                    (r, slot, ("V", k, b, c))))
+                if special:
+                    v_issued = specials + 1
+                self.copy(r, own if special else self.kv_full[slot], (r, slot, ("V", k, b, c)))
+                issued = at
             specials += special
 
         for k, (n, _, whole, _) in enumerate(self.items):
             if not self.fp8 and k > 0:  # (the first item's by the helper)
                 yield self.q_empty[r].done(k - 1)
-                self.load_q(r)
+                if not abort[r]:
+                    self.load_q(r)
+                    q_issued = k + 1
             yield from load_k(k, 0)
             for b in range(n):
                 if b + 1 < n:
@@ -167,9 +195,28 @@ class Model:
             if whole:
                 for _ in range(STAGE):
                     slot = yield from take()
-                    self.kv_full[slot].arrive()
-                self.stage_free[r].arrive()
+                    if not abort[r]:
+                        self.kv_full[slot].arrive()
+                if not abort[r]:
+                    self.stage_free[r].arrive()
             yield None
+        if not abort[r]:
+            return
+        # waits for the copies in flight: the last use of each barrier
+        if not self.count_issued:  # (planted: counts what an abort has passed over too)
+            v_issued, q_issued = specials, len(self.items)
+        waits = [(self.v_full[r][c % SLOTS], c // SLOTS) for c in range(max(0, v_issued - SLOTS), v_issued)]
+        if r == 0:
+            waits += [(self.kv_full[c % SLOTS], c // SLOTS) for c in range(max(0, issued - SLOTS), issued)]
+            if not self.fp8:
+                waits.append((self.q_full, q_issued - 1))
+        for bar, phase in waits:
+            expect(bar.phase >= phase, "in flight", "a wait for nothing", bar.name, phase, bar.phase)
+        # (the second CTA's on the first's barriers: given time to land)
+        for bar, what, cta, phase in self.copies:
+            expect(cta != r or (bar, phase) in waits or (r == 1 and bar.name not in [x.name for x in self.v_full[1]]),
+                   "in flight", bar.name, what)
+        self.copies = [x for x in self.copies if x[2] != r]
 
     def mma(self):
         at = t0 = 0
@@ -183,6 +230,9 @@ class Model:
                 slot = at % SLOTS
                 yield self.kv_full[slot].done(at // SLOTS)
                 at += 1
+                if self.abort[0]:
+                    continue
+
                 def work(slot=slot, c=c):
                     for r in range(2):
                         expect(self.ring[r][slot] == ("K", k, b, c), "K", self.ring[r][slot], k, b)
@@ -191,7 +241,8 @@ class Model:
                         if c == self.ks - 1:
                             self.s_buf[r][t & 1] = [("S", t)] * len(WARPS)
                 self.tensor.append([work, *free(slot)])
-            self.tensor.append([self.s_full[r][t & 1].arrive for r in range(2)])
+            if not self.abort[0]:
+                self.tensor.append([self.s_full[r][t & 1].arrive for r in range(2)])
 
         def outputs(k, b, t):
             nonlocal at
@@ -203,6 +254,8 @@ class Model:
             if b == 0 and k > 0:
                 yield self.o_free.done(k - 1)
             yield self.p_full[t & 1].done(t >> 1)
+            if self.abort[0]:
+                return
             for c, slot in enumerate(slots):
                 def work(slot=slot, c=c):
                     for r in range(2):
@@ -218,7 +271,7 @@ class Model:
             for b in range(n):
                 if b + 1 < n:
                     yield from products(k, b + 1, t0 + b + 1)
-                if b + 1 == n and not self.fp8:
+                if b + 1 == n and not self.fp8 and not self.abort[0]:
                     self.tensor.append([self.q_empty[r].arrive for r in range(2)])
                 if b + 1 == n and whole:
                     for c in range(STAGE):
@@ -280,6 +333,8 @@ class Model:
             yield self.pv_done[r][(t0 - 1) & 1].done((t0 - 1) >> 1)
             expect(self.o[r] == (k, n - 1), "result", k, self.o[r])
             bad = self.bad[r][k & 1][half]
+            if self.numbered and bad != k + 1:
+                bad = 0
             expect(bad == (k + 1 if self.has_bad(half, k) else 0), "flag", k, bad)
             yield None
             self.o_free.arrive()
@@ -288,11 +343,12 @@ class Model:
                     slot = (at + 2 * half + c) % SLOTS
                     held = self.ring[r][slot] or ("O", k, ())
                     expect(held[:2] == ("O", k), "stage", k, held)
-                    self.ring[r][slot] = ("O", k, (*held[2], quad))
+                    if held[:2] == ("O", k):
+                        self.ring[r][slot] = ("O", k, (*held[2], quad))
                 at += STAGE
                 yield None
                 self.staged[r].arrive()
-            if bad:
+            if bad and not self.numbered:
                 yield self.late[r][half].sync()
                 if quad == 0:
                     self.bad[r][k & 1][half] = 0
@@ -307,6 +363,8 @@ class Model:
                 v_at = at + self.ks + b * (self.ks + self.vs) + (self.ks if b + 1 < n else 0)
                 yield self.v_full[r][specials % SLOTS].done(specials // SLOTS)
                 specials += 1
+                if self.abort[r]:
+                    break
                 bad |= self.chance(.4, "bad", r, k, b)
                 if bad:
                     for x in range(2):
@@ -320,25 +378,38 @@ class Model:
             if whole:
                 yield self.staged[r].done(tiles)
                 tiles += 1
+                if self.abort[r]:
+                    continue
                 for c in range(STAGE):
                     slot = (at + c) % SLOTS
-                    held = self.ring[r][slot]
+                    held = self.ring[r][slot] or (None,)
                     expect(held[:2] == ("O", k) and sorted(held[2]) == list(range(QUADS)), "store", k, held)
                     yield None
                     self.kv_empty[r][slot].arrive()
                 at += STAGE
 
     def run(self):
-        roles = [self.mma()]
+        Bar.strict = self.abort_at is None
+        roles, cta = [self.mma()], [0]
         for r in range(2):
             roles += [self.producer(r), self.helper(r)]
             roles += [self.softmax(r, w) for w in range(len(WARPS))]
+            cta += [r] * (2 + len(WARPS))
         waits = [None] * len(roles)
         weight = [self.rng.choice([1, 1, 5, 20]) for _ in roles]
         tensor, copies = (self.rng.choice([1, 5, 20]) for _ in range(2))
         alive = set(range(len(roles)))
+        turn = 0
         while alive or self.tensor or self.copies:
-            ready = [i for i in sorted(alive) if waits[i] is None or waits[i]()]
+            turn += 1
+            if turn == self.abort_at:
+                self.abort[self.rng.randrange(2)] = True
+            ready = [i for i in sorted(alive)
+                     if waits[i] is None or (self.abort[cta[i]] and hasattr(waits[i], "bar")) or waits[i]()]
+            if not ready and not self.tensor and not self.copies and True in self.abort:
+                expect(False in self.abort, "hang", self.items)
+                self.abort[:] = [True, True]  # (the other CTA's waits run out as well)
+                continue
             odds = [weight[i] for i in ready]
             if self.tensor:
                 ready, odds = ready + ["tensor"], odds + [tensor]
@@ -350,7 +421,7 @@ class Model:
                 for step in self.tensor.pop(0):
                     step()
             elif which == "copy":
-                bar, what = self.copies.pop(self.rng.randrange(len(self.copies)))
+                bar, what, _, _ = self.copies.pop(self.rng.randrange(len(self.copies)))
                 if what is not None:
                     self.ring[what[0]][what[1]] = what[2]
                 bar.complete()
@@ -390,3 +461,21 @@ def test_the_model_sees_sums_that_overwrite_maxima():
 def test_the_model_sees_one_array_of_exponents():
     with pytest.raises(Fault, match="exponent"):
         schedules(250, True, two_exponents=False)
+
+
+def aborts(count, fp8, **layout):
+    for seed in range(count):
+        rng = random.Random(seed)
+        items = random_items(rng)
+        Model(seed, fp8, items, abort_at=rng.randint(1, 40 * sum(i[0] for i in items)), **layout).run()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_an_aborted_pair_comes_to_its_end(fp8):
+    aborts(250, fp8)
+
+
+def test_the_model_sees_flags_that_are_put_back_behind_a_barrier():
+    # (after an abort some warps may see the flag and some not)
+    with pytest.raises(Fault, match="hang"):
+        aborts(1000, False, numbered=False)
