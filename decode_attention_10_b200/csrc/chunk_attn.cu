@@ -76,6 +76,7 @@ constexpr int kTileCost = 3;  // a tile's fixed cost, in blocks (Q, first softma
 constexpr int kPartCost = 2;  // what a second part in a pair costs over a tile's start, in blocks
 constexpr int kMaxShared = 128;  // (pairs of SMs, at most)
 static_assert(2 * kMaxShared >= kMaxAttnGrid, "every pair");
+constexpr uint64_t kLandNs = 1000000;  // by when a copy in flight has landed (they take ~1 us)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
@@ -702,12 +703,16 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
   const bool leader = elect_one();
   const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
   const int page_shift = kPaged ? 31 - __clz(a.page_size) : 0;
-  uint32_t chunk = 0, issued = 0, specials = 0;
+  uint32_t chunk = 0, specials = 0;
+  // what has been issued: uses of slots, special blocks' V, items' Q (the first by the helper)
+  uint32_t issued = 0, v_issued = 0;
+  int q_issued = 1;
   int item = 0;
   Cursor cur;
   cur.init(S.plan, a.batch, g);
   Item it, nx;
   bool has = cur.next(it);
+  const bool any = has;
   if (!kPaged && has && leader) {
     prefetch_tensormap(&chunk_maps(a.kv[it.b])->k);
     prefetch_tensormap(&chunk_maps(a.kv[it.b])->v);
@@ -717,7 +722,10 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
     if constexpr (!kFp8) {
       if (item > 0) {  // (the first item's Q is loaded by the helper warp meanwhile)
         mbar_wait(&S.q_empty, (item - 1) & 1, abort);
-        if (leader && !*abort) load_q(S, q_map, a, it, rank);
+        if (leader && !*abort) {
+          load_q(S, q_map, a, it, rank);
+          q_issued = item + 1;
+        }
       }
     }
     // one tile of the sequence reads its rows once; several find them in L2
@@ -785,6 +793,7 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
             remote_arrive_expect_tx(bar, kSlotBytes);
           else if (c == 0)
             mbar_arrive_expect_tx(own, C::kVSlots * kSlotBytes);
+          if (special) v_issued = specials + 1;
           issued = chunk;
         }
         if (special) bar = smem_u32(own);
@@ -826,14 +835,22 @@ __device__ void run_producer(Smem& S, const CUtensorMap* q_map, const ChunkAttnA
     ++item;
   }
   // Before the CTAs may exit, every copy must have landed (after an abort; else all were used):
-  // those of both CTAs that the pair's barriers count are waited for in the first.
-  if (*abort && leader) {
-    if (rank == 0)
-      for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c)
-        mbar_wait_drain(&S.kv_full[c % kSlots], (c / kSlots) & 1);
-    for (uint32_t c = specials > kSlots ? specials - kSlots : 0; c < specials; ++c)
-      mbar_wait_drain(&S.v_full[c % kSlots], (c / kSlots) & 1);
-    if (!kFp8 && rank == 0 && item > 0) mbar_wait_drain(&S.q_full, (item - 1) & 1);
+  // those that the pair's barriers count are waited for in the first CTA, as far as both have
+  // issued them. A wait that gives up has been long enough for all of them; the second CTA
+  // cannot see those barriers and waits a while.
+  if (*abort && leader && any) {
+    bool wait = true;
+    for (uint32_t c = v_issued > kSlots ? v_issued - kSlots : 0; c < v_issued && wait; ++c)
+      wait = mbar_wait_drain(&S.v_full[c % kSlots], (c / kSlots) & 1);
+    if (rank == 0) {
+      for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued && wait; ++c)
+        wait = mbar_wait_drain(&S.kv_full[c % kSlots], (c / kSlots) & 1);
+      if (!kFp8 && wait) mbar_wait_drain(&S.q_full, (q_issued - 1) & 1);
+    } else {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < kLandNs) {
+      }
+    }
   }
   __syncwarp();
 }

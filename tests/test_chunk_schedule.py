@@ -34,7 +34,7 @@ class Fault(AssertionError):
 
 
 def expect(ok, *what):
-    if not ok and (Bar.strict or what[0] == "hang"):
+    if not ok and (Bar.strict or what[0] in ("hang", "in flight")):
         raise Fault(what)
 
 
@@ -471,7 +471,7 @@ def aborts(count, fp8, **layout):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
-def test_an_aborted_pair_comes_to_its_end(fp8):
+def test_an_aborted_cta_waits_for_its_copies_in_flight(fp8):
     aborts(250, fp8)
 
 
@@ -479,3 +479,8 @@ def test_the_model_sees_flags_that_are_put_back_behind_a_barrier():
     # (after an abort some warps may see the flag and some not)
     with pytest.raises(Fault, match="hang"):
         aborts(1000, False, numbered=False)
+
+
+def test_the_model_sees_waits_for_copies_that_were_not_issued():
+    with pytest.raises(Fault, match="in flight"):
+        aborts(250, False, issued=False)
