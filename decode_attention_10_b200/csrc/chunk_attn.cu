@@ -27,10 +27,13 @@
 //               in log2 (4 for FP8), so O is rarely rescaled; the pair of warps that shares 32
 //               rows agrees on that with one barrier a block. Sums in float32, of the
 //               unrounded weights.
-// FP8 caches: the codes go to the tensor cores as they are (kind::f8f6f4). Q and P become
-// pairs of e4m3 matrices, high part and rounded remainder, both accumulated into the same S
-// or O: twice the products at twice the rate, and half the bytes of K and V. Q's scale is a
-// power of two per row. P is kept below 2^8 by adding 4 to its exponent.
+// FP8 caches: the codes go to the tensor cores as they are (kind::f8f6f4). Q becomes a pair of
+// e4m3 matrices, high part and rounded remainder, P an e4m3 and an e5m2 matrix (split_weights),
+// both accumulated into the same S or O: twice the products at twice the rate, and half the bytes
+// of K and V. Q's scale is a power of two per row. P is 2^8 where the score is the running maximum
+// and below 2^12 everywhere. (With 2^8.75 as the limit no weight would need its e5m2 part first, but
+// the running maximum would rise more often: 957 us instead of 846 for two prompts of 1500 over
+// 4500, where e4m3 pairs up to 2^8 took 808.)
 //
 // Work split: tiles of all sequences laid end to end, each costing its blocks plus
 // kTileCost; pair g takes the g-th of G equal contiguous ranges, so causal chunks, prompts
@@ -78,13 +81,14 @@ constexpr int kMaxShared = 128;  // (pairs of SMs, at most)
 static_assert(2 * kMaxShared >= kMaxAttnGrid, "every pair");
 constexpr uint64_t kLandNs = 1000000;  // by when a copy in flight has landed (they take ~1 us)
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kIdescE5m2A = 1u << 7;  // kind::f8f6f4: A's format is e5m2 (0: e4m3)
 
 template <bool kFp8>
 struct Cfg {
   static constexpr int kKSlots = kFp8 ? 1 : 2;  // ring slots of a CTA's half of a K block
   static constexpr int kVSlots = kFp8 ? 1 : 2;
   static constexpr float kRescale = kFp8 ? 4.0f : 8.0f;  // log2 units
-  static constexpr float kPExp = kFp8 ? 4.0f : 0.0f;     // P = 2^(s - m + kPExp)
+  static constexpr float kPExp = kFp8 ? 8.0f : 0.0f;     // P = 2^(s - m + kPExp)
   static constexpr uint32_t kIdescS = idesc_f16(256, kBlock, !kFp8, false, false);
   static constexpr uint32_t kIdescPV = idesc_f16(256, kHeadDim, !kFp8, false, true);
 };
@@ -919,8 +923,8 @@ __device__ void run_mma(Smem& S, const ChunkAttnArgs& a, int g, uint32_t tmem) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int part = i >> 2, kt = i & 3;  // 32 keys each
-            pair_mma_ts<true>(d, p + 32 * part + 8 * kt, v_lo[c] + 4096 * kt / 16, C::kIdescPV,
-                              !(first && i == 0));
+            pair_mma_ts<true>(d, p + 32 * part + 8 * kt, v_lo[c] + 4096 * kt / 16,
+                              part == 0 ? C::kIdescPV : C::kIdescPV | kIdescE5m2A, !(first && i == 0));
           }
         } else {
 #pragma unroll
@@ -1021,6 +1025,27 @@ __device__ __forceinline__ void split_e4m3x2(uint32_t v, uint32_t& hi, uint32_t&
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(rest));
   hi = h;
   lo = l;
+}
+// Weights (f16x2, 0 <= v < 2^12) as sums of an e4m3 and an e5m2 value: from 256 up the value's first
+// three bits as e5m2 and the rest (at most 256) as e4m3, below e4m3 and the rest as e5m2. Either
+// way the sum is within 2^-8 of the value's power of two, down to 2^-6; below, the rest is at most
+// 2^-10 and off by at most 1/8 of itself or 2^-17. (An e4m3 rest has no step below 2^-9, and a row
+// of one large weight and thousands of small ones, which an e4m3 pair rounded to nothing, lost all
+// of the small ones: 80 % of the result at 65,536 keys, 0.1 % so.)
+__device__ __forceinline__ void split_weights(uint32_t v, uint32_t& e4, uint32_t& e5) {
+  uint32_t large, rest, back;
+  uint16_t a, b;
+  asm("set.ge.u32.f16x2 %0, %1, %2;" : "=r"(large) : "r"(v), "r"(0x5C005C00u));
+  // (e5m2 is f16's first byte)
+  const uint32_t first = (v + 0x00800080u) & 0xFF00FF00u & large;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(v), "r"(first));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(rest));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(v), "r"(back));
+  // (what e4m3 left of a large one does not reach its first three bits)
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(rest));
+  e4 = a;
+  e5 = b;
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -1375,14 +1400,14 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
         l += l0 + l1;
       }
       if constexpr (kFp8) {
-        uint32_t hl[32];  // 16 words of high parts, 16 of low parts
+        uint32_t hl[32];  // 16 words of e4m3 parts, 16 of e5m2 parts
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          uint32_t h0, l0, h1, l1w;
-          split_e4m3x2(pw[2 * i], h0, l0);
-          split_e4m3x2(pw[2 * i + 1], h1, l1w);
-          hl[i] = h0 | (h1 << 16);
-          hl[16 + i] = l0 | (l1w << 16);
+          uint32_t a0, b0, a1, b1;
+          split_weights(pw[2 * i], a0, b0);
+          split_weights(pw[2 * i + 1], a1, b1);
+          hl[i] = a0 | (a1 << 16);
+          hl[16 + i] = b0 | (b1 << 16);
         }
         uint32_t w0[16], w1[16];
 #pragma unroll

@@ -335,7 +335,9 @@ MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, c
  * see (later tokens, rows past the sequence's end) may hold any bytes, infinities and NaN
  * included, and do not reach its result. For FP8 caches the cached codes are used exactly, q
  * as in mfa_decode_attn with one power-of-two scale per token and head, and the softmax weights
- * as e4m3 pairs within 2^-8 of their value or 2^-14 of the row's largest weight.
+ * as sums of an e4m3 and an e5m2 value: down to 2^-14 of the row's largest weight within 2^-8
+ * (and 2^-11, an f16's) of their value, below within 1/8 of it or 2^-25 of the largest, up or
+ * down, so that thousands of such weights still add up.
  * q, out: device bf16 [n_rows, 64, 256], not overlapping; scale: positive, a normal float.
  * kv: a table of mfa_chunk_table_bytes(kv->batch) bytes or more.
  * ws: device workspace of mfa_chunk_workspace_bytes(kv->batch) bytes (initialized once).

@@ -387,3 +387,52 @@ def test_results_over_the_queries_are_refused():
     b = Batch([5], [40], False, 64, seed=26)
     with pytest.raises(mfa.MfaError, match="INVALID_ARG"):
         mfa.chunk_attn(b.q, b.cache(), b.q_start, b.seq_lens, out=b.q)
+
+
+@KV
+@pytest.mark.parametrize("new", [1, 301], ids=["parts", "tiles"])
+@pytest.mark.parametrize("keys,score", [(8192, 10), (32768, 11), (65536, 12), (65536, 14)])
+def test_a_dominating_key_leaves_the_others_their_weight(fp8, new, keys, score):
+    # The first key has half to nine tenths of every row's weight and a value of zero; the rest of the
+    # weight is spread over thousands of keys with values around 1.
+    b = Batch([new], [keys - new], fp8, 0, seed=28)
+    if fp8:
+        b.k_scale, b.v_scale = 1.0, 1.0 / 16
+    g = torch.Generator().manual_seed(29)
+    k = torch.randn(keys, DIM, generator=g)
+    k[:, 0], k[0] = 0.0, 0.0
+    k[0, 0] = 16.0 * score  # q . k / 16, with a 1 in q
+    v = 1.0 + 0.5 * torch.randn(keys, DIM, generator=g)
+    v[0] = 0.0
+    b.k[0].copy_(k / b.k_scale)
+    b.v[0].copy_(v / b.v_scale)
+    b.q[:, :, 0] = 1.0
+    out = run(b).double()
+    kd, vd = b.values("k", 0), b.values("v", 0)
+    for t in sorted({0, 3, new // 2, new - 1} & set(range(new))):
+        end = keys - new + t + 1
+        q = b.q[t].double()
+        s = q @ kd[:end].T / 16
+        p = torch.softmax(s, -1)
+        want = p @ vd[:end]
+        top = p.amax(-1, keepdim=True)
+        assert (top > 0.4).all() and (want > 0.05).all()
+        # Each weight's rounding to bf16: half a step, 2^-8 of it. FP8: a weight of w = 2^8 p / top
+        # or more is an f16 (2^-11) and then e4m3 + e5m2: from 2^-6 up within 2^-8 of its power of
+        # two; below, the e5m2 part is at most 2^-10, off by 2^-14 at most, and by 2^-3 of itself or
+        # half of the smallest step, 2^-17.
+        one = (2.0 ** -8 + 2.0 ** -11) * p
+        if fp8:
+            one = one + torch.minimum(2.0 ** -22 * top, 2.0 ** -3 * p + 2.0 ** -25 * top)
+        # These errors have either sign: within 8 standard deviations of their sum, a step's error
+        # taken as its largest, and a mean of at most 2^-6 of the weights' sum (steps of up to a
+        # quarter of a weight, (1/4)^2 / 12 times the few that a density falls by over a weight).
+        off = 8 * (one ** 2 @ vd[:end] ** 2).sqrt() + (2.0 ** -6 if fp8 else 0) * (p @ vd[:end].abs())
+        # the scores' float32 sums, and FP8 q as a pair (chunk_util); the result's rounding
+        dot = (q.abs() @ kd[:end].abs().T).amax(-1, keepdim=True) / 16
+        err = 256 * 2.0 ** -23 * dot
+        if fp8:
+            err = err + 2.0 ** -17 * q.abs().amax(-1, keepdim=True) * kd.abs().sum(-1).max() / 16
+        tol = 2.0 ** -8 * want.abs() + off + 2 * err * (p @ vd[:end].abs() + want.abs())
+        d = (out[t] - want).abs()
+        assert (d <= tol).all(), (t, float(d.max()), float(tol.min()), float((d / want).max()))
