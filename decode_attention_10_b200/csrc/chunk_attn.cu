@@ -1106,11 +1106,12 @@ __device__ __noinline__ void split_q(Smem& S, const ChunkAttnArgs& a, const Item
     for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // 128 <= mx 2^-e < 256; e >= -100 keeps 2^-e finite; a row with an infinity (its scores are
-    // NaN anyhow) and one of zeros take 0. (A subnormal mx counts as 2^-127.)
+    // 128 <= mx 2^-e < 256; e >= -100 keeps 2^-e finite; a row of zeros takes 0. (A subnormal mx
+    // counts as 2^-127.) A row with an infinity becomes NaN: its scores are infinities or NaN, which
+    // e4m3 has no infinity to form, and their softmax is NaN whatever the keys.
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
     const int e = mx > 0.f && ex < 255 ? max(ex - 127 - 7, -100) : 0;
-    const float sc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const float sc = ex < 255 ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
     if (part == 0) S.q_exp[parity][r] = e;
     uint32_t hi[4], lo[4];
 #pragma unroll

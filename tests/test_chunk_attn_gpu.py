@@ -436,3 +436,19 @@ def test_a_dominating_key_leaves_the_others_their_weight(fp8, new, keys, score):
         tol = 2.0 ** -8 * want.abs() + off + 2 * err * (p @ vd[:end].abs() + want.abs())
         d = (out[t] - want).abs()
         assert (d <= tol).all(), (t, float(d.max()), float(tol.min()), float((d / want).max()))
+
+
+@KV
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("new,cached", [(1, 0), (1, 129), (6, 100), (6, 9000), (66, 3)])
+def test_a_query_with_an_infinity_is_nan(fp8, new, cached, bad):
+    # inf times any key is an infinity or NaN, so the row has no softmax
+    b = Batch([new], [cached], fp8, 64, seed=30)
+    clean = run(b)
+    t = new // 2
+    b.q[t, 3, 5] = b.q[new - 1, 63, 255] = bad
+    out = run(b)
+    keep = torch.ones(new, HEADS, dtype=torch.bool)
+    keep[t, 3] = keep[new - 1, 63] = False
+    assert out[t, 3].isnan().all() and out[new - 1, 63].isnan().all()
+    assert torch.equal(out[keep], clean[keep])
