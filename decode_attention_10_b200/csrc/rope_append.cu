@@ -133,10 +133,20 @@ __global__ void __launch_bounds__(kThreads)
   if (a.positions != nullptr && tid < pairs)
     pos = a.positions[static_cast<size_t>(a.pair_axis[tid]) * a.n_rows + row];
   // the token's sequence: as many as end at or before this row (one round trip; sequences
-  // without new tokens end where they begin and are passed over)
+  // without new tokens end where they begin and are passed over). Every block looks all ranges of
+  // rows over: where they do not hold together, none writes.
   int seq = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads)
-    seq += __syncthreads_count(b0 + tid < a.batch && a.q_start[b0 + tid + 1] <= row);
+  bool layout = false;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    bool ends = false;
+    if (b0 + tid < a.batch) {
+      const int s0 = a.q_start[b0 + tid], s1 = a.q_start[b0 + tid + 1];
+      layout |= s0 < 0 || s1 < s0 || s1 > a.n_rows;
+      ends = s1 <= row;
+    }
+    seq += __syncthreads_count(ends);
+  }
+  if (layout && row == 0) atomicOr(a.err, kErrLayout);
   if (seq >= a.batch || row < a.q_start[seq]) return;  // the row belongs to no sequence
   const KvSeq* kv = a.kv + seq;
   const int place = a.seq_lens[seq] - (a.q_start[seq + 1] - row);  // the cache row
@@ -149,8 +159,9 @@ __global__ void __launch_bounds__(kThreads)
     s_sin[tid] = t[pairs + tid];
   }
   // (also the barrier before the angles are read)
-  if (__syncthreads_or(bad_pos || at < 0)) {
-    if (tid == 0) atomicOr(a.err, kErrCapacity);
+  if (__syncthreads_or(bad_pos || at < 0 || layout)) {
+    const bool refused = __syncthreads_or(layout);
+    if (tid == 0 && !refused) atomicOr(a.err, kErrCapacity);
     return;
   }
   float c[8], s[8];

@@ -320,7 +320,8 @@ typedef struct {
  * A token whose row j or page lies outside the cache, or whose position is outside
  * [0, max_pos), writes nothing (neither q_out nor the cache) and sets MFA_ERR_CAPACITY; so
  * does every token of a sequence with seq_lens[b] < n_b that would fall on a negative row.
- * Only the appended rows of the cache are written. */
+ * A q_start that is not nondecreasing within [0, n_rows]: nothing is written, and
+ * MFA_ERR_INVALID_ARG is set. Only the appended rows of the cache are written. */
 MFA_API mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, const void* v,
                                    int32_t v_ld, const mfa_rope* rope, const int32_t* positions,
                                    const mfa_kv_cache* kv, const int32_t* q_start,

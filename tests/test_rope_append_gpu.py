@@ -293,3 +293,39 @@ def test_prompt_in_chunks_then_decoding(fp8, page):
         # bf16 step of it, 2^-7, on few elements; its scores move by 2^-7 of a product's share)
         d = (o.to(F64) - ref).abs()
         assert (d <= 2 * tol + 2e-3).all(), float((d - tol).max())
+
+
+@KV
+@pytest.mark.parametrize("more", [0, 190], ids=["few", "many"])
+def test_ranges_that_do_not_hold_together_write_nothing(fp8, more):
+    from decode_attention_10_b200 import mfa
+    b = Batch([2, 3, 4, 2 + more], [50, 60, 0, 200], fp8, 64, seed=10, spare=200)
+    rope, pair_axis = make_rope()
+    k, v = new_rows(b.rows, 10)
+    cache, ws = b.cache(), mfa.Workspace(4)
+    n, before = b.rows, snapshot(b)
+    for starts in ([0, 2, 5, 9, n + 29], [-3, 2, 5, 9, n], [0, 2, 1, 4, n], [0, 2, 5, n + 900, n],
+                   [0, 2, 5, 9, n + 1], [1, 0, 5, 9, n], [0, n, n, n, n - 1]):
+        q_start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        q_out = torch.full_like(b.q, 9.0)
+        mfa.rope_append(b.q, k, v, cache, q_start, b.seq_lens, rope, q_out=q_out, ws=ws)
+        assert mfa.get_error(ws) == 1 and (q_out == 9.0).all(), starts
+        mfa.rope_append(None, k, v, cache, q_start, b.seq_lens, ws=ws)
+        assert mfa.get_error(ws) == 1, starts
+        assert all(torch.equal(x, y) for x, y in zip(snapshot(b), before)), starts
+    q_out = mfa.rope_append(b.q, k, v, cache, b.q_start, b.seq_lens, rope, ws=ws)
+    assert mfa.get_error(ws) == 0
+    verify(b, before, q_out, k, v, rope, pair_axis, None)
+
+
+def test_a_bad_range_behind_many_sequences_is_seen():
+    from decode_attention_10_b200 import mfa
+    for more in (0, 300):  # (both kernels; the last range is a later round of a block's threads)
+        b = Batch([more] + [0] * 1022 + [3], [0] + [5] * 1023, False, 64, seed=11, spare=8)
+        k, v = new_rows(b.rows, 11)
+        cache, ws, before = b.cache(), mfa.Workspace(1024), snapshot(b)
+        q_start = b.q_start.clone()
+        q_start[1024] += 1
+        mfa.rope_append(None, k, v, cache, q_start, b.seq_lens, ws=ws)
+        assert mfa.get_error(ws) == 1
+        assert all(torch.equal(x, y) for x, y in zip(snapshot(b), before))
