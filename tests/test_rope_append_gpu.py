@@ -329,3 +329,120 @@ def test_a_bad_range_behind_many_sequences_is_seen():
         mfa.rope_append(None, k, v, cache, q_start, b.seq_lens, ws=ws)
         assert mfa.get_error(ws) == 1
         assert all(torch.equal(x, y) for x, y in zip(snapshot(b), before))
+
+
+# Appends of more tokens than SMs run with fewer threads a block, each with more heads: the same
+# forms on both sides of that choice.
+ROWS = pytest.mark.parametrize("rows", [148, 149, 401])
+
+
+@KV
+@ROWS
+@pytest.mark.parametrize("page", [0, 64], ids=["buffers", "p64"])
+@pytest.mark.parametrize("rot,axes,interleaved", [(256, 1, False), (256, 3, True), (64, 2, False),
+                                                  (208, 4, True), (16, 1, True), (96, 3, False)])
+def test_rotated_append_of_few_and_many_tokens(fp8, rows, page, rot, axes, interleaved):
+    from decode_attention_10_b200 import mfa
+    new = [1, 0, rows - 75, 70, 3, 1]
+    b = Batch(new, [64, 9, 100, 0, 31, 255], fp8, page, seed=rot + axes, spare=3)
+    rope, pair_axis = make_rope(rot, axes, interleaved)
+    k, v = new_rows(rows, rot)
+    positions = None
+    if axes > 1:
+        positions = torch.randint(0, 4096, (axes, rows), dtype=torch.int32, device="cuda",
+                                  generator=torch.Generator("cuda").manual_seed(2))
+        positions[:, 0], positions[:, rows - 1] = 0, 4095
+    before = snapshot(b)
+    ws = mfa.Workspace(b.batch)
+    q_out = mfa.rope_append(b.q, k, v, b.cache(), b.q_start, b.seq_lens, rope, positions, ws=ws)
+    assert mfa.get_error(ws) == 0
+    verify(b, before, q_out, k, v, rope, pair_axis, positions)
+
+
+@KV
+@ROWS
+@pytest.mark.parametrize("rot", [256, 128])
+def test_in_place_and_append_only_of_few_and_many_tokens(fp8, rows, rot):
+    from decode_attention_10_b200 import mfa
+    b = Batch([rows - 2, 2], [30, 200], fp8, 64, seed=rot)
+    rope, _ = make_rope(rot)
+    k, v = new_rows(rows, 2)
+    want = mfa.rope_append(b.q, k, v, b.cache(), b.q_start, b.seq_lens, rope)
+    appended = [b.stored(which, i)[b.cached[i]:].view(torch.uint8).clone()
+                for which in "kv" for i in range(2)]
+    q = b.q.clone()
+    assert mfa.rope_append(q, k, v, b.cache(), b.q_start, b.seq_lens, rope, q_out=q) is q
+    assert torch.equal(q, want)
+    for buf in (b.k, b.v):
+        buf.view(torch.uint8)[:] = 0
+    assert mfa.rope_append(None, k, v, b.cache(), b.q_start, b.seq_lens, rope) is None
+    again = [b.stored(which, i)[b.cached[i]:].view(torch.uint8) for which in "kv" for i in range(2)]
+    assert all(torch.equal(x, y) for x, y in zip(again, appended))
+
+
+@KV
+@ROWS
+def test_append_without_rotation_of_few_and_many_tokens(fp8, rows):
+    from decode_attention_10_b200 import mfa
+    b = Batch([rows - 66, 66], [61, 0], fp8, 64, seed=5)
+    k, v = new_rows(rows, 5, ld=520)
+    mfa.rope_append(None, k, v, b.cache(), b.q_start, b.seq_lens)
+    for i in range(2):
+        part = slice(b.starts[i], b.starts[i + 1])
+        for which, src, s in (("k", k, b.k_scale), ("v", v, b.v_scale)):
+            got = b.stored(which, i)[b.cached[i]:]
+            if fp8:
+                want = (src[part].float() / s).clamp(-448, 448).to(torch.float8_e4m3fn)
+                assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+            else:
+                assert torch.equal(got, src[part])
+
+
+@KV
+@ROWS
+def test_rows_of_no_sequence_stay_with_few_and_many_tokens(fp8, rows):
+    from decode_attention_10_b200 import mfa
+    b = Batch([2, rows - 7], [10, 70], fp8, 64, seed=6, lead=1, behind=4)
+    rope, pair_axis = make_rope()
+    k, v = new_rows(rows, 6)
+    before = snapshot(b)
+    q_out = torch.full_like(b.q, 9.0)
+    mfa.rope_append(b.q, k, v, b.cache(), b.q_start, b.seq_lens, rope, q_out=q_out)
+    verify(b, before, q_out, k, v, rope, pair_axis, None)
+    assert (q_out[:1] == 9.0).all() and (q_out[b.starts[-1]:] == 9.0).all()
+
+
+@KV
+@ROWS
+def test_bad_tokens_write_nothing_among_few_and_many(fp8, rows):
+    from decode_attention_10_b200 import mfa
+    b = Batch([2, rows - 2], [62, 60], fp8, 64, seed=7)
+    rope, pair_axis = make_rope(rot=128, axes=2, interleaved=True, max_pos=1000)
+    k, v = new_rows(rows, 7)
+    cache, ws = b.cache(), mfa.Workspace(2)
+    good = torch.arange(rows, dtype=torch.int32, device="cuda").repeat(2, 1).contiguous()
+
+    def call(lens=None, positions=good):
+        q_out = torch.full_like(b.q, 9.0)
+        mfa.rope_append(b.q, k, v, cache, b.q_start, b.seq_lens if lens is None else lens, rope,
+                        positions, q_out=q_out, ws=ws)
+        return (q_out == 9.0).flatten(1).all(1).nonzero().flatten().tolist(), mfa.get_error(ws)
+
+    assert call() == ([], 0)
+    cap = b.per_seq[1] * 64
+    # the second sequence ends two past its pages, or begins three before its first row
+    assert call(lens=torch.tensor([64, cap + 2], dtype=torch.int32, device="cuda")) == \
+        ([rows - 2, rows - 1], 3)
+    assert call(lens=torch.tensor([64, rows - 5], dtype=torch.int32, device="cuda")) == ([2, 3, 4], 3)
+    for axis, row, p in ((0, 1, -1), (1, rows - 1, 1000), (0, rows - 2, 2 ** 31 - 1), (1, 0, -2 ** 31)):
+        pos = good.clone()
+        pos[axis, row] = p
+        assert call(positions=pos) == ([row], 3)
+    before, old = snapshot(b), b.table.clone()
+    page = (60 + 40) // 64  # holds positions 64 .. 127 of the second sequence
+    for bad in (10 ** 6, -1):
+        b.table[1, page] = bad
+        lost, err = call()
+        assert err == 3 and lost == list(range(2 + 64 - 60, 2 + min(128 - 60, rows - 2)))
+        b.table.copy_(old)
+        assert all(torch.equal(x, y) for x, y in zip(snapshot(b), before))  # (the others' as before)
