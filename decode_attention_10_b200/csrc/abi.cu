@@ -48,11 +48,12 @@ bool encode_rows(CUtensorMap* m, void* base, int rows, int dtype, int box_rows) 
   return encode_2d(m, base, (uint64_t)rows, kHeadDim, elem, 128 / elem, box_rows);
 }
 
-// whether two arrays of `bytes` bytes overlap
-bool overlap(const void* a, const void* b, size_t bytes) {
+// whether arrays of a_bytes and b_bytes bytes overlap
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return (x < y ? y - x : x - y) < bytes;
+  return x < y ? y - x < a_bytes : x - y < b_bytes;
 }
+bool overlap(const void* a, const void* b, size_t bytes) { return overlap(a, bytes, b, bytes); }
 
 // a device array of int32
 bool valid_ints(const int32_t* p) {
@@ -605,6 +606,13 @@ mfa_status mfa_rope_append(const void* q, const void* k, int32_t k_ld, const voi
     std::memcpy(a.pair_axis, rope->pair_axis, sizeof(a.pair_axis));
   } else if (q != nullptr || positions != nullptr) {
     return MFA_ERR_INVALID_ARG;
+  }
+  // (q_out is written while other tokens' keys and values are still read)
+  const auto span = [&](int32_t ld) { return ((size_t)(n_rows - 1) * ld + kHeadDim) * 2; };
+  if (q_out != nullptr) {
+    const size_t q_bytes = (size_t)n_rows * kHeads * kHeadDim * 2;
+    if (overlap(q_out, q_bytes, k, span(k_ld)) || overlap(q_out, q_bytes, v, span(v_ld)))
+      return MFA_ERR_INVALID_ARG;
   }
   WsLayout L;
   st = check_ws(ws, ws_bytes, kv->batch, &L);

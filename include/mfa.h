@@ -311,7 +311,8 @@ typedef struct {
  *   q: device bf16 [n_rows, 64, 256] or NULL (append only); q_out: as q, not overlapping it,
  *   or q itself.
  *   k, v: device bf16, row t at element t * k_ld (v_ld); k_ld and v_ld are multiples of 8,
- *   at least 256, so that k and v may be halves of one projection's output.
+ *   at least 256, so that k and v may be halves of one projection's output. q_out and the
+ *   cache rows that are written do not overlap them (from k's first row to its last, for q_out).
  *   rope: host pointer, NULL = no rotation (then q must be NULL: nothing would happen to it).
  *   positions: device int32 [rope->n_axes, n_rows], or NULL for rope->n_axes == 1: the
  *   position of a token is then its cache row j. NULL without rope.

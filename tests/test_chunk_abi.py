@@ -172,3 +172,26 @@ def test_plain_rotation_turns_pairs(interleaved):
         assert (y[..., a] - z.real).abs().max() < 1e-12
         assert (y[..., b] - z.imag).abs().max() < 1e-12
     assert torch.equal(y[..., 48:], x[..., 48:])
+
+
+def test_rotated_queries_over_the_new_keys_or_values_are_refused(lib):
+    rope = mfa.RopeDesc(4096, 10, 256, 0, 1, (ctypes.c_uint8 * 128)())
+    q, out, k, v = 1 << 30, 2 << 30, 3 << 30, 4 << 30
+    n, ld = 5, 512
+    q_bytes, span = n * 64 * 256 * 2, ((n - 1) * ld + 256) * 2
+
+    def call(q=q, out=out, k=k, v=v):
+        # (a workspace of no size: a call that passes the checks before it is refused for that,
+        # or for the lack of a device)
+        return lib.mfa_rope_append(P(q), P(k), ld, P(v), ld, ctypes.byref(rope), None, kv(), FAKE, FAKE,
+                                   n, P(out), FAKE, 0, None)
+
+    assert call() in (4, 5) and call(out=q) in (4, 5)
+    assert call(k=v - 512) in (4, 5)  # halves of one projection
+    for which in ("k", "v"):
+        for at in (out, out + 16, out + q_bytes - 16, out - 16, out - span + 16):
+            assert call(**{which: at}) == 1, (which, at - out)
+        for at in (out + q_bytes, out - span):
+            assert call(**{which: at}) in (4, 5)
+        assert call(out=q, **{which: q + 32}) == 1  # in place
+        assert call(out=out, **{which: q + 32}) in (4, 5)  # (the queries are only read)
