@@ -109,26 +109,40 @@ _chunk = None  # mfa_torch: the chunk calls for torch tensors (csrc/binding.cpp)
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libmfa.so and mfa_torch.so (once). Raises if they have not been built."""
-    global _lib, _chunk
+    """Load libmfa.so (once). Raises if it has not been built."""
+    global _lib
     if _lib is not None:
         return _lib
-    for p in (path, BINDING_PATH):
-        if not os.path.exists(p):
-            raise RuntimeError(f"{p} is missing: build it with "
-                               "`python -m decode_attention_10_b200.build`")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m decode_attention_10_b200.build`")
     lib = ctypes.CDLL(path)
     for name, (res, args) in _SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    spec = importlib.util.spec_from_file_location("mfa_torch", BINDING_PATH)
-    chunk = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(chunk)
-    chunk.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                 for f in (lib.mfa_rope_append, lib.mfa_chunk_attn)))
-    _lib, _chunk = lib, chunk
+    _lib = lib
     return lib
+
+
+def _load_chunk():
+    """Load mfa_torch.so (once), which only the chunk calls need. Raises if it has not been
+    built, or for another torch."""
+    global _chunk
+    if _chunk is not None:
+        return
+    lib, how = load(), "build it with `python -m decode_attention_10_b200.build`"
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is missing: {how}")
+    try:
+        spec = importlib.util.spec_from_file_location("mfa_torch", BINDING_PATH)
+        chunk = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(chunk)
+        chunk.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                     for f in (lib.mfa_rope_append, lib.mfa_chunk_attn)))
+    except ImportError as e:
+        raise RuntimeError(f"{BINDING_PATH} does not fit torch {torch.__version__}: {how}") from e
+    _chunk = chunk
 
 
 def _check(status: int, where: str):
@@ -427,8 +441,8 @@ def rope_append(q, k, v, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
     (q_out; q itself may be given). Rows q_start[b] .. q_start[b + 1] are sequence b's, the
     last of its seq_lens[b] positions; k and v may be views with spaced rows. positions: int32
     [axes, T] or [T]; None: a token's cache row."""
-    if _lib is None:
-        load()
+    if _chunk is None:
+        _load_chunk()
     batch = cache.batch
     if q is None:
         if q_out is not None:
@@ -462,8 +476,8 @@ def chunk_attn(q, cache, q_start: torch.Tensor, seq_lens: torch.Tensor,
     """mfa_chunk_attn: causal attention of a ragged batch of new tokens q [T, 64, 256] over the
     cache (which holds their keys and values already); rows as in rope_append. Rows of no
     sequence are left as they were in `out`. ws: a ChunkWorkspace."""
-    if _lib is None:
-        load()
+    if _chunk is None:
+        _load_chunk()
     batch = cache.batch
     if out is None:
         with _made_on(stream):

@@ -195,3 +195,20 @@ def test_rotated_queries_over_the_new_keys_or_values_are_refused(lib):
             assert call(**{which: at}) in (4, 5)
         assert call(out=q, **{which: q + 32}) == 1  # in place
         assert call(out=out, **{which: q + 32}) in (4, 5)  # (the queries are only read)
+
+
+def test_decode_calls_need_no_binding(lib, monkeypatch, tmp_path):
+    monkeypatch.setattr(mfa, "_lib", None)
+    monkeypatch.setattr(mfa, "_chunk", None)
+    monkeypatch.setattr(mfa, "BINDING_PATH", str(tmp_path / "mfa_torch.so"))
+    assert mfa.load().mfa_version() == lib.mfa_version()
+    ws = type("W", (), {"addr": 4096, "nbytes": BIG, "device_index": 0})()
+    desc = mfa.KvCacheDesc(2, 0, 1.0, 1.0, 4096, 0)
+    cache = type("C", (), {"batch": 2, "addr": ctypes.addressof(desc), "device_index": 0})()
+    q = torch.zeros(4, 64, 256, dtype=torch.bfloat16)
+    starts, lens = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(RuntimeError, match="mfa_torch.so is missing: build it"):
+        mfa.chunk_attn(q, cache, starts, lens, out=q, ws=ws)
+    (tmp_path / "mfa_torch.so").write_bytes(b"of another torch")
+    with pytest.raises(RuntimeError, match="does not fit torch .*build it"):
+        mfa.rope_append(None, q, q, cache, starts, lens, ws=ws)
