@@ -17,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmfa.so")
 BINDING = os.path.join(HERE, "mfa_torch.so")
+BINDING_FOR = os.path.join(ROOT, "_build", "mfa_torch.txt")
 SOURCES = ["abi.cu", "query_path.cu", "gemm_tc.cu", "attention_tc.cu", "out_proj.cu", "noalloc.cu",
            "selftest.cu", "split_plan.cu", "rope_append.cu", "chunk_attn.cu"]
 HEADERS = ["mfa_internal.cuh", "attn_plan.cuh", "sm100.cuh", "chunk.cuh"]
@@ -45,13 +46,24 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _built_for() -> str:
+    """What the binding was last built for (see build_binding)."""
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
+    import torch
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src, os.path.join(ROOT, "include", "mfa.h"), os.path.abspath(__file__)]
-    if (not force and os.path.exists(BINDING)
+    # it fits one torch and one Python only
+    built_for = f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}\n"
+    if (not force and os.path.exists(BINDING) and _built_for() == built_for
             and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)):
         return BINDING
-    import torch
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"),
            os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -67,6 +79,10 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
+    with open(tmp, "w") as f:
+        f.write(built_for)
+    os.replace(tmp, BINDING_FOR)
     return BINDING
 
 

@@ -212,3 +212,24 @@ def test_decode_calls_need_no_binding(lib, monkeypatch, tmp_path):
     (tmp_path / "mfa_torch.so").write_bytes(b"of another torch")
     with pytest.raises(RuntimeError, match="does not fit torch .*build it"):
         mfa.rope_append(None, q, q, cache, starts, lens, ws=ws)
+
+
+def test_binding_is_built_again_for_another_torch(monkeypatch, tmp_path):
+    from decode_attention_10_b200 import build
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "mfa_torch.so"))
+    monkeypatch.setattr(build, "BINDING_FOR", str(tmp_path / "built" / "mfa_torch.txt"))
+    compiled = []
+
+    def compiler(cmd, check):
+        compiled.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("binding")
+
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    for version, builds in (("1.0", 1), ("1.0", 1), ("2.0", 2), ("2.0", 2), ("1.0", 3)):
+        monkeypatch.setattr(torch, "__version__", version)
+        build.build_binding()
+        assert len(compiled) == builds, version
+    build.os.remove(build.BINDING_FOR)  # (nobody knows what it was built for)
+    build.build_binding()
+    assert len(compiled) == 4
