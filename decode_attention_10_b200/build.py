@@ -80,6 +80,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
     os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
+    tmp = f"{BINDING_FOR}.{os.getpid()}.tmp"
     with open(tmp, "w") as f:
         f.write(built_for)
     os.replace(tmp, BINDING_FOR)
