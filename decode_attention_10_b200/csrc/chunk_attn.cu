@@ -1378,7 +1378,9 @@ __device__ void run_softmax(Smem& S, const ChunkAttnArgs& a, int g, uint32_t ran
           }
         }
       }
-      // weights 2^(s - base); a hidden key's score is -inf and its weight 0. All exponentials go
+      // weights 2^(s - base); a hidden key's score is -inf and its weight 0. They are rounded to what
+      // the tensor cores read: bf16, off by at most 2^-8 of themselves, up or down (FP8: f16, 2^-11,
+      // then split_weights); their sum is of the float32 values. All exponentials go
       // through the special-function unit, which they keep busy for half of a block's products:
       // a quarter of them by polynomial made the softmax shorter and long calls 2 to 4 %
       // slower, since those run at the power limit and the polynomial takes more of it.
