@@ -452,3 +452,21 @@ def test_a_query_with_an_infinity_is_nan(fp8, new, cached, bad):
     keep[t, 3] = keep[new - 1, 63] = False
     assert out[t, 3].isnan().all() and out[new - 1, 63].isnan().all()
     assert torch.equal(out[keep], clean[keep])
+
+
+@KV
+@pytest.mark.parametrize("rise", [0.3, 1.5, 2.5, 2.7, 2.8, 4.0, 5.4, 5.6])
+def test_scores_above_the_running_maximum(fp8, rise):
+    # later keys score up to `rise` above the first block's, below and above what raises the running
+    # maximum (4 in log2, 2.77, for FP8; 8, 5.55, for bf16): weights of up to 2^12, or 2^8
+    b = Batch([1, 6], [1500, 1500], fp8, 0, seed=31)
+    b.k_scale = 1.0 / 64 if fp8 else 1.0
+    g = torch.Generator().manual_seed(32)
+    for i in range(2):
+        up = torch.rand(b.total[i], generator=g) * rise
+        up[:128], up[700] = 0.0, rise
+        k = 0.05 * torch.randn(b.total[i], DIM, generator=g)
+        k[:, 0] = up
+        b.k[i].copy_((k / b.k_scale).clamp(-448, 448))
+    b.q[:, :, 0] = 16.0
+    check(run(b), b)
